@@ -83,6 +83,10 @@ typedef enum nvpa_status {
                                      exceeded its time limit (2 s); outputs are incomplete;
                                      never expected in correct operation                    */
 
+/* Element type of a KV cache (cache_type arguments). */
+#define NVPA_CACHE_BF16 0
+#define NVPA_CACHE_E4M3 1          /* 8-bit codes with scales, see nvpa_store_kvcache_fp8 */
+
 /* Library version, as 10000*major + 100*minor + patch. */
 int nvpa_version(void);
 
@@ -401,6 +405,125 @@ nvpa_status_t nvpa_gather_kv(void* dst, const void* cache,
                              const int32_t* cu_seqlens_k, int batch, int total_k,
                              int num_kv_heads, int head_dim, int num_blocks, int block_size,
                              int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * nvpa_store_kvcache_fp8 -- nvpa_store_kvcache into an 8-bit cache: each row of head_dim
+ * values (one token, one KV head, K or V) is quantised to e4m3 codes with one power-of-two
+ * scale as it is written.  (No page describes this: it is an addition, half the bytes of the
+ * bf16 cache.)  With amax the row's largest finite magnitude,
+ *     e      = max(-118, ceil(log2(amax / 448)))
+ *     code_d = x_d * 2^-e rounded to the nearest e4m3 value (ties to even)
+ *     scale byte = e + 127
+ * so no finite value saturates and code_d * 2^e is exact in bf16 (for magnitudes below
+ * 1.9375 * 2^127, above which rounding up leaves bf16's range).  An infinity or a NaN is
+ * stored as the code of NaN (0x7f) and does not count in amax.
+ *
+ *   k, v            bf16, token strides as in nvpa_store_kvcache.
+ *   k_cache,v_cache e4m3 (one byte per value) pools [num_blocks, block_size, num_kv_heads,
+ *                   head_dim], contiguous, 16-byte aligned (written).
+ *   k_scales,       uint8 [num_blocks, num_kv_heads, block_size], contiguous, 16-byte
+ *   v_scales        aligned (written): the scale of slot b * block_size + row and head h is
+ *                   byte (b * num_kv_heads + h) * block_size + row.
+ *   slot_mapping    as in nvpa_store_kvcache (-1: padding; out of range: flagged, skipped;
+ *                   two tokens with the same slot: undefined which row lands).
+ *   head_dim        64 or 128; block_size 16, 32, 64, 128 or 256.
+ * Errors: NVPA_ERR_INVALID_ARG, NVPA_ERR_UNSUPPORTED as for nvpa_store_kvcache.
+ */
+nvpa_status_t nvpa_store_kvcache_fp8(const void* k, const void* v, int64_t k_token_stride,
+                                     int64_t v_token_stride, void* k_cache, void* v_cache,
+                                     uint8_t* k_scales, uint8_t* v_scales, const int32_t* slot_mapping,
+                                     int num_tokens, int num_kv_heads, int head_dim, int num_blocks,
+                                     int block_size, int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * nvpa_gather_kv_fp8 -- nvpa_gather_kv from one pool of an 8-bit cache: dst rows are
+ * code * 2^(scale byte - 127) as bf16 (exact for every row that nvpa_store_kvcache_fp8
+ * writes).  Scale bytes are read as they are: valid ones are 9 .. 247.
+ *
+ *   dst             bf16 [total_k, num_kv_heads, head_dim] (written).  Rows whose block id is
+ *                   out of range are zeroed and flagged; rows from cu_seqlens_k[batch] on
+ *                   are left as they are and flagged (NVPA_FLAG_BAD_LENGTH).
+ */
+nvpa_status_t nvpa_gather_kv_fp8(void* dst, const void* cache, const uint8_t* scales,
+                                 const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* cu_seqlens_k, int batch, int total_k, int num_kv_heads,
+                                 int head_dim, int num_blocks, int block_size, int32_t* err_flag,
+                                 cudaStream_t stream);
+
+/*
+ * Workspace for nvpa_paged_decode_attention_window, in bytes, for the same arguments
+ * (host-side values only; 0 for invalid arguments).
+ */
+size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                               int max_context_len, int block_size, int window, int num_sinks,
+                                               int num_splits);
+
+/*
+ * nvpa_paged_decode_attention_window -- nvpa_paged_decode_attention over a bf16 or an e4m3
+ * cache, with a sliding window and first tokens that stay visible.  (No page describes the
+ * window or the 8-bit cache: additions.)  The query of sequence b is at position
+ * p = context_lens[b] - 1 and sees key j <= p iff
+ *     window == 0,  or  j > p - window  (the last `window` keys, its own among them),
+ *     or  j < num_sinks.
+ * Only rows of visible keys are read, and only the block-table entries of blocks that hold a
+ * visible key: blocks that fell out of the window may have been freed (their entries may
+ * hold anything).
+ *
+ *   cache_type      NVPA_CACHE_BF16 (k_scales = v_scales = NULL) or NVPA_CACHE_E4M3.
+ *   window          >= 0, 0 = no window;  num_sinks >= 0 (no effect without a window).
+ *   num_splits      0 = automatic; n > 0 = at most n partitions of what a query can see.
+ *   workspace       at least nvpa_paged_decode_window_workspace_size(...) bytes, 256-byte
+ *                   aligned; calls that share a workspace must not overlap.
+ *   other arguments, out, lse and errors as for nvpa_paged_decode_attention.
+ * The softmax weights are rounded to 16 significant bits (bf16 cache) or 11 (e4m3 cache)
+ * before the product with the values; sums are float32.
+ */
+nvpa_status_t nvpa_paged_decode_attention_window(
+    void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,
+    const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+    int block_size, int max_context_len, float softmax_scale, int window, int num_sinks, int num_splits,
+    void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * Workspace for nvpa_chunk_attention, in bytes, for the same arguments (host-side values
+ * only; 0 for invalid arguments).
+ */
+size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
+                                           int head_dim, int max_seqlen_q, int max_context_len, int block_size,
+                                           int window, int num_sinks, int num_splits);
+
+/*
+ * nvpa_chunk_attention -- attention of a chunk of new tokens per sequence over a bf16 or an
+ * e4m3 paged cache: chunked prefill (hundreds of tokens over a long cache), checking draft
+ * tokens (a few), or whole prompts.  Sequence i owns query rows cu_seqlens_q[i] ..
+ * cu_seqlens_q[i+1]-1, its newest Lq tokens; its keys 0 .. context_lens[i]-1 (the new tokens
+ * stored first) are read through block_tables[i].  Query row r is at position
+ * context_lens[i] - Lq + r; which keys a position sees (causal, window, sinks), and which
+ * block-table entries are read, is as for nvpa_paged_decode_attention_window.  When there
+ * are few query rows the keys are cut into partitions that run in parallel and are merged
+ * with their log-sum-exp weights.
+ *
+ *   out             bf16 [total_q, num_q_heads, head_dim] (written); rows from
+ *                   cu_seqlens_q[batch] on are left as they are.
+ *   lse_out         float32 [total_q, num_q_heads] (written) or NULL.
+ *   q               bf16 [total_q, num_q_heads, head_dim], contiguous.
+ *   cu_seqlens_q    int32 [batch + 1], non-decreasing.
+ *   context_lens    int32 [batch] with 0 <= Lq <= context_lens[i] <= max_context_len,
+ *                   Lq <= max_seqlen_q, context_lens[i] <= max_blocks_per_seq*block_size,
+ *                   cu_seqlens_q[i+1] <= total_q.  A violation is flagged
+ *                   (NVPA_FLAG_BAD_LENGTH) and that sequence's rows are left unwritten.
+ *   max_seqlen_q,   host-side upper bounds (they size the partitioning).
+ *   max_context_len
+ *   other arguments as for nvpa_paged_decode_attention_window.
+ */
+nvpa_status_t nvpa_chunk_attention(
+    void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,
+    const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* cu_seqlens_q, const int32_t* context_lens, int batch, int total_q, int max_seqlen_q,
+    int max_context_len, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size,
+    float softmax_scale, int window, int num_sinks, int num_splits, void* workspace, size_t workspace_bytes,
+    int32_t* err_flag, cudaStream_t stream);
 
 /*
  * nvpa_check_bounded_wait -- test helper for the tensor-core kernels' time-bounded waits:

@@ -16,15 +16,21 @@ from ._lib import (  # noqa: F401
 )
 from .api import (  # noqa: F401
     check_bounded_wait,
+    chunk_attention,
+    chunk_attention_workspace_size,
     decode_shared_prefix_workspace_size,
     decode_step,
     decode_step_shared_prefix,
     gather_kv,
+    gather_kv_fp8,
     lse_combine,
     paged_decode_attention,
+    paged_decode_attention_window,
     paged_decode_partial,
+    paged_decode_window_workspace_size,
     paged_decode_workspace_size,
     store_kvcache,
+    store_kvcache_fp8,
     varlen_prefill_attention,
     varlen_prefill_workspace_size,
 )

@@ -25,6 +25,9 @@ NVPA_FLAG_BAD_BLOCK_ID = 2
 NVPA_FLAG_BAD_LENGTH = 4
 NVPA_FLAG_TIMEOUT = 8
 
+NVPA_CACHE_BF16 = 0
+NVPA_CACHE_E4M3 = 1
+
 # Every function the header declares, with (restype, argtypes).
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -55,6 +58,16 @@ SIGNATURES = {
     "nvpa_varlen_prefill_attention": (_i, [_p, _p, _p, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i,
                                            _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p, _p]),
     "nvpa_gather_kv": (_i, [_p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _i, _p, _p]),
+    "nvpa_store_kvcache_fp8": (_i, [_p, _p, _i64, _i64, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p,
+                                    _p]),
+    "nvpa_gather_kv_fp8": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _i, _p, _p]),
+    "nvpa_paged_decode_window_workspace_size": (_sz, [_i] * 9),
+    "nvpa_paged_decode_attention_window": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _p, _i, _i,
+                                                _i, _i, _i, _i, _i, _f, _i, _i, _i, _p, _sz, _p,
+                                                _p]),
+    "nvpa_chunk_attention_workspace_size": (_sz, [_i] * 11),
+    "nvpa_chunk_attention": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i,
+                                  _i, _i, _i, _i, _i, _f, _i, _i, _i, _p, _sz, _p, _p]),
     "nvpa_check_bounded_wait": (_i, [_p, _p]),
 }
 

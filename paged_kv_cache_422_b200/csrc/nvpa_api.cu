@@ -362,6 +362,146 @@ nvpa_status_t nvpa_gather_kv(void* dst, const void* cache, const int32_t* block_
                          num_kv_heads, head_dim, num_blocks, block_size, err_flag, stream);
 }
 
+nvpa_status_t nvpa_store_kvcache_fp8(const void* k, const void* v, int64_t k_token_stride,
+                                     int64_t v_token_stride, void* k_cache, void* v_cache,
+                                     uint8_t* k_scales, uint8_t* v_scales, const int32_t* slot_mapping,
+                                     int num_tokens, int num_kv_heads, int head_dim, int num_blocks,
+                                     int block_size, int32_t* err_flag, cudaStream_t stream) {
+    g_last_error[0] = 0;
+    NVPA_REQUIRE(num_tokens >= 0, NVPA_ERR_INVALID_ARG, "num_tokens < 0");
+    nvpa_status_t st = check_attention_shapes(num_kv_heads, num_kv_heads, head_dim, num_blocks, block_size, 1);
+    if (st != NVPA_OK) return st;
+    if (num_tokens == 0) return NVPA_OK;
+    NVPA_REQUIRE(k && v && k_cache && v_cache && k_scales && v_scales && slot_mapping, NVPA_ERR_INVALID_ARG,
+                 "null pointer");
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    NVPA_REQUIRE(k_token_stride >= row && v_token_stride >= row, NVPA_ERR_INVALID_ARG,
+                 "token stride smaller than num_kv_heads*head_dim");
+    NVPA_REQUIRE(k_token_stride % 8 == 0 && v_token_stride % 8 == 0, NVPA_ERR_INVALID_ARG,
+                 "token strides must be multiples of 8 elements (16 bytes)");
+    NVPA_REQUIRE(aligned16(k) && aligned16(v) && aligned16(k_cache) && aligned16(v_cache) &&
+                     aligned16(k_scales) && aligned16(v_scales),
+                 NVPA_ERR_INVALID_ARG, "k, v, cache and scale pointers must be 16-byte aligned");
+    return run_store_kvcache_fp8(k, v, k_token_stride, v_token_stride, k_cache, v_cache, k_scales, v_scales,
+                                 slot_mapping, num_tokens, num_kv_heads, head_dim, num_blocks, block_size,
+                                 err_flag, stream);
+}
+
+nvpa_status_t nvpa_gather_kv_fp8(void* dst, const void* cache, const uint8_t* scales,
+                                 const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* cu_seqlens_k, int batch, int total_k, int num_kv_heads,
+                                 int head_dim, int num_blocks, int block_size, int32_t* err_flag,
+                                 cudaStream_t stream) {
+    g_last_error[0] = 0;
+    NVPA_REQUIRE(batch >= 0 && total_k >= 0, NVPA_ERR_INVALID_ARG, "sizes must be >= 0");
+    nvpa_status_t st = check_attention_shapes(num_kv_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                                              max_blocks_per_seq);
+    if (st != NVPA_OK) return st;
+    if (batch == 0 || total_k == 0) return NVPA_OK;
+    NVPA_REQUIRE(dst && cache && scales && block_tables && cu_seqlens_k, NVPA_ERR_INVALID_ARG, "null pointer");
+    NVPA_REQUIRE(aligned16(dst) && aligned16(cache) && aligned16(scales), NVPA_ERR_INVALID_ARG,
+                 "dst, cache and scales must be 16-byte aligned");
+    return run_gather_kv_fp8(dst, cache, scales, block_tables, max_blocks_per_seq, cu_seqlens_k, batch,
+                             total_k, num_kv_heads, head_dim, num_blocks, block_size, err_flag, stream);
+}
+
+// The checks that the windowed decode and the chunk attention share; *empty is set when
+// there is nothing to do.
+static nvpa_status_t check_window_call(const WindowCall& c, int cache_type, bool* empty) {
+    *empty = false;
+    NVPA_REQUIRE(c.batch >= 0 && c.total_q >= 0 && c.max_seqlen_q >= 0 && c.max_context_len >= 0 &&
+                     c.num_splits >= 0,
+                 NVPA_ERR_INVALID_ARG, "sizes and num_splits must be >= 0");
+    NVPA_REQUIRE(c.window >= 0 && c.num_sinks >= 0, NVPA_ERR_INVALID_ARG,
+                 "window and num_sinks must be >= 0");
+    NVPA_REQUIRE(cache_type == NVPA_CACHE_BF16 || cache_type == NVPA_CACHE_E4M3, NVPA_ERR_INVALID_ARG,
+                 "cache_type must be NVPA_CACHE_BF16 or NVPA_CACHE_E4M3");
+    nvpa_status_t st = check_attention_shapes(c.hq, c.hkv, c.head_dim, c.num_blocks, c.block_size,
+                                              c.max_blocks_per_seq);
+    if (st != NVPA_OK) return st;
+    NVPA_REQUIRE(std::isfinite(c.scale), NVPA_ERR_INVALID_ARG, "softmax_scale not finite");
+    NVPA_REQUIRE((long long)c.total_q * c.hq <= 0x7fffffffLL, NVPA_ERR_UNSUPPORTED,
+                 "query rows times num_q_heads above 2^31-1");
+    if (c.batch == 0 || c.total_q == 0) {
+        *empty = true;
+        return NVPA_OK;
+    }
+    NVPA_REQUIRE(c.out && c.q && c.k_cache && c.v_cache && c.block_tables && c.context_lens && c.workspace,
+                 NVPA_ERR_INVALID_ARG, "null pointer");
+    NVPA_REQUIRE(aligned16(c.out) && aligned16(c.q) && aligned16(c.k_cache) && aligned16(c.v_cache),
+                 NVPA_ERR_INVALID_ARG, "bf16 and cache pointers must be 16-byte aligned");
+    if (cache_type == NVPA_CACHE_E4M3)
+        NVPA_REQUIRE(c.k_scales && c.v_scales && aligned16(c.k_scales) && aligned16(c.v_scales),
+                     NVPA_ERR_INVALID_ARG, "an e4m3 cache needs 16-byte aligned k_scales and v_scales");
+    else
+        NVPA_REQUIRE(!c.k_scales && !c.v_scales, NVPA_ERR_INVALID_ARG,
+                     "k_scales and v_scales must be null for a bf16 cache");
+    NVPA_REQUIRE((reinterpret_cast<uintptr_t>(c.workspace) & 255u) == 0, NVPA_ERR_INVALID_ARG,
+                 "workspace must be 256-byte aligned");
+    return NVPA_OK;
+}
+
+static bool window_sizes_ok(int hq, int hkv, int head_dim, int max_context_len, int window, int num_sinks,
+                            int num_splits) {
+    return hq > 0 && hkv > 0 && hq % hkv == 0 && hq / hkv <= 8 && (head_dim == 64 || head_dim == 128) &&
+           max_context_len >= 0 && window >= 0 && num_sinks >= 0 && num_splits >= 0;
+}
+
+size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                               int max_context_len, int block_size, int window, int num_sinks,
+                                               int num_splits) {
+    if (batch < 0 || !attn_block_size_ok(block_size) ||
+        !window_sizes_ok(num_q_heads, num_kv_heads, head_dim, max_context_len, window, num_sinks, num_splits))
+        return 0;
+    return row_attention_workspace_bytes(batch, batch, 1, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                         block_size, window, num_sinks, num_splits);
+}
+
+nvpa_status_t nvpa_paged_decode_attention_window(
+    void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,
+    const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+    int block_size, int max_context_len, float softmax_scale, int window, int num_sinks, int num_splits,
+    void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream) {
+    g_last_error[0] = 0;
+    const WindowCall c{out, lse_out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                       max_blocks_per_seq, nullptr, context_lens, batch, batch, 1, max_context_len,
+                       num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, softmax_scale, window,
+                       num_sinks, num_splits, workspace, workspace_bytes, err_flag};
+    bool empty;
+    const nvpa_status_t st = check_window_call(c, cache_type, &empty);
+    return st != NVPA_OK || empty ? st : run_row_attention(c, stream);
+}
+
+size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
+                                           int head_dim, int max_seqlen_q, int max_context_len, int block_size,
+                                           int window, int num_sinks, int num_splits) {
+    if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || !attn_block_size_ok(block_size) ||
+        !window_sizes_ok(num_q_heads, num_kv_heads, head_dim, max_context_len, window, num_sinks, num_splits))
+        return 0;
+    return row_attention_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
+                                         max_context_len, block_size, window, num_sinks, num_splits);
+}
+
+nvpa_status_t nvpa_chunk_attention(
+    void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,
+    const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* cu_seqlens_q, const int32_t* context_lens, int batch, int total_q, int max_seqlen_q,
+    int max_context_len, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size,
+    float softmax_scale, int window, int num_sinks, int num_splits, void* workspace, size_t workspace_bytes,
+    int32_t* err_flag, cudaStream_t stream) {
+    g_last_error[0] = 0;
+    const WindowCall c{out, lse_out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                       max_blocks_per_seq, cu_seqlens_q, context_lens, batch, total_q, max_seqlen_q,
+                       max_context_len, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                       softmax_scale, window, num_sinks, num_splits, workspace, workspace_bytes, err_flag};
+    bool empty;
+    const nvpa_status_t st = check_window_call(c, cache_type, &empty);
+    if (st != NVPA_OK || empty) return st;
+    NVPA_REQUIRE(cu_seqlens_q != nullptr, NVPA_ERR_INVALID_ARG, "null pointer");
+    return run_row_attention(c, stream);
+}
+
 nvpa_status_t nvpa_check_bounded_wait(int32_t* err_flag, cudaStream_t stream) {
     g_last_error[0] = 0;
     NVPA_REQUIRE(err_flag != nullptr, NVPA_ERR_INVALID_ARG, "err_flag must not be null");

@@ -44,6 +44,29 @@ struct DecodeCall {
     float* out_f32 = nullptr;
 };
 
+// Attention with a sliding window and sinks over a bf16 or e4m3 cache: one query token per
+// sequence (cu_seqlens_q null, total_q == batch) or a chunk of them.
+struct WindowCall {
+    void* out;
+    float* lse_out;
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const uint8_t* k_scales;       // null: bf16 cache
+    const uint8_t* v_scales;
+    const int32_t* block_tables;
+    int max_blocks_per_seq;
+    const int32_t* cu_seqlens_q;
+    const int32_t* context_lens;
+    int batch, total_q, max_seqlen_q, max_context_len;
+    int hq, hkv, head_dim, num_blocks, block_size;
+    float scale;
+    int window, num_sinks, num_splits;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t* err_flag;
+};
+
 struct PrefillCall {
     void* out;
     float* lse_out;
@@ -113,6 +136,18 @@ nvpa_status_t run_gather_kv(void* dst, const void* cache, const int32_t* block_t
                             int max_blocks_per_seq, const int32_t* cu_seqlens_k, int batch,
                             int total_k, int hkv, int head_dim, int num_blocks, int block_size,
                             int32_t* err_flag, cudaStream_t stream);
+nvpa_status_t run_store_kvcache_fp8(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                    void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales,
+                                    const int32_t* slot_mapping, int num_tokens, int hkv, int head_dim,
+                                    int num_blocks, int block_size, int32_t* err_flag, cudaStream_t stream);
+nvpa_status_t run_gather_kv_fp8(void* dst, const void* cache, const uint8_t* scales,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* cu_seqlens_k, int batch, int total_k, int hkv, int head_dim,
+                                int num_blocks, int block_size, int32_t* err_flag, cudaStream_t stream);
+// Few query rows per KV head (row_attention.cu).
+size_t row_attention_workspace_bytes(int batch, int total_q, int max_q, int hq, int hkv, int head_dim,
+                                     int max_ctx, int block_size, int window, int sinks, int num_splits);
+nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream);
 nvpa_status_t run_bounded_wait_check(int32_t* err_flag, cudaStream_t stream);
 
 }  // namespace nvpa

@@ -1,0 +1,840 @@
+// Attention of a few query rows per KV head over a bf16 or e4m3 paged cache, with an
+// optional sliding window and first tokens that stay visible: the decode step (one token
+// per sequence) and short chunks of new tokens.
+//
+// Mathematics.  Query token at position p sees key j iff j <= p and (no window, or
+// j > p - window, or j < sinks).  Per query row: s_j = scale <q, k_j> over its visible
+// keys, out = sum_j softmax(s)_j v_j, lse = log sum_j exp(s_j), in one pass with a running
+// maximum and sum.  An e4m3 row is c * 2^e (fp8.cuh): the key's 2^e multiplies its score
+// in float32, the value's 2^e its weight.
+//
+// Bound by the bytes of the visible keys and values (2 G flop per bf16 byte, 4 G per e4m3
+// byte for G query heads per KV head).  The products are small matrix products over the G
+// heads, so they go to warp-level MMAs with the keys as the M dimension and the query rows
+// as N = 8: S^T[16 keys, 8 rows] = K Q^T and O^T[D, 8 rows] += V^T P^T.  With CUDA-core
+// products the e4m3 cache's instructions per byte would bound the kernel; with MMAs 16 keys
+// take about 300 warp instructions for either cache and any G up to 8.  (tcgen05 needs M =
+// 64 or 128 rows of accumulators in TMEM per product, a single warp's stream of keys has no
+// use for it.)
+//
+// Layout.  Every warp is an independent worker: it takes items (KV head, row tile, range of
+// 16-key tiles of one sequence) and streams their K and V through its own ring of shared
+// memory stages with 16-byte cp.async copies.  Rows that no query row of the item sees are
+// zero-filled and never read, and neither are the block-table entries of blocks without a
+// visible key: blocks that fell out of the window may be freed.  A row's 16-byte chunks are
+// XOR-swizzled by its key so that the fragment loads below hit all banks.
+//   K fragment (A of S^T, keys x dims): the MMA's k index may be any order of the dims as
+//     long as Q's fragment has the same, so lane (g, t) = (lane / 4, lane % 4) reads whole
+//     16-byte chunks of keys g and g + 8.
+//   V fragment (A of O^T, dims x keys): bf16 through ldmatrix.trans; e4m3 by loading 16
+//     (D = 128) or 8 dims of the lane's four keys and interleaving pairs of keys with prmt.
+//   P^T (B of O^T): the scores lie with keys in rows; movmatrix transposes 8 x 8 tiles.
+// Rounding: an e4m3 code is exact in fp16; q is scaled by a power of two per row to at most
+// 1 in magnitude and rounded to fp16 (an error of 2^-25 of the row's largest element at
+// most: bf16 has 8 significant bits).  Weights are fp16 for the e4m3 cache (2^-11 relative)
+// and a sum of two bf16 (2^-17) for the bf16 cache, whose values are used as they are.
+// The fp16 weight includes the value's 2^e and is taken relative to the largest such weight
+// so far (a running maximum of its own beside the softmax's), so a scale of any size neither
+// overflows nor is lost beside larger ones.
+#include <algorithm>
+#include <cuda_fp16.h>
+#include <mutex>
+
+#include "decode_params.cuh"
+#include "fp8.cuh"
+
+namespace nvpa {
+
+namespace {
+
+constexpr int kRowWarps = 4;
+
+struct RowParams {
+    const uint16_t* q;           // [total_q, hq, D]
+    const void* k_cache;
+    const void* v_cache;
+    const uint8_t* k_scales;     // [num_blocks, hkv, block_size] (e4m3 cache)
+    const uint8_t* v_scales;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* cu_q;         // null: one query token per sequence
+    uint16_t* out;
+    float* lse_out;
+    float* o_part;
+    float* lse_part;
+    int4* items;                 // two int4 per item
+    int32_t* nsplit;             // [total_q] partitions of each query token, 0: none
+    int32_t* counter;            // [0] items claimed after the first round, [1] items
+    int32_t* err;
+    int batch, total_q, max_q, hq, hkv, group;
+    int max_blocks, num_blocks, block_size, block_shift;
+    int max_ctx;
+    int window, sinks;           // window 0: none
+    int tok;                     // query tokens per row tile
+    int row_tiles;               // row tiles of the longest chunk
+    int chunk;                   // 16-key tiles per partition
+    int s_max;
+    int max_entries;             // entries that the item table holds
+    float scale_log2;
+};
+
+// The 16-key tiles that the queries at positions [p0, p1] see, as one virtual range: `head`
+// tiles from key 0 on (the sinks), then those from key 16 * (head + skip) on.
+struct TileRange {
+    int head, skip, count;
+};
+__device__ __forceinline__ TileRange tile_range(int p0, int p1, int window, int sinks) {
+    TileRange r;
+    const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
+    const int first = lo / kTileKeys;
+    r.head = min(first, (int)(((long long)min(sinks, p0) + kTileKeys - 1) / kTileKeys));
+    r.skip = first - r.head;
+    r.count = r.head + p1 / kTileKeys + 1 - first;
+    return r;
+}
+
+// Bit i set for the first n of 16 keys.
+__device__ __forceinline__ uint32_t first_keys(int n) {
+    return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+// Keys key0 .. key0 + 15 that a query at position p sees (p < 0: none).
+__device__ __forceinline__ uint32_t seen_keys(int key0, int p, int window, int sinks) {
+    uint32_t m = first_keys(p + 1 - key0);
+    if (window > 0) m &= ~first_keys(p - window + 1 - key0) | first_keys(sinks - key0);
+    return m;
+}
+
+// ------------------------------------------------------------------------------------
+// plan: context lengths -> items, full partitions first, then the shorter ones, longest
+// first (as the decode plan orders them)
+// ------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
+    __shared__ int warp_tot[32];
+    __shared__ int s_cls[kLengthClasses];
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    for (int i = tid; i < kLengthClasses; i += blockDim.x) s_cls[i] = 0;
+    if (p.cu_q != nullptr)
+        for (int i = tid; i < p.total_q; i += blockDim.x) p.nsplit[i] = 0;
+    __syncthreads();
+    const int lim = (int)min((long long)p.max_ctx, (long long)p.max_blocks * p.block_size);
+    struct Tile {
+        int b, q0, ntok, p0, tiles, ns;
+    };
+    // row tile i: (sequence, tile of its query tokens); ntok = 0 when there is none
+    auto tile = [&](int i, bool flag) {
+        Tile t;
+        t.b = i / p.row_tiles;
+        const int rt = i - t.b * p.row_tiles;
+        int ctx = __ldg(p.context_lens + t.b), lq = 1;
+        t.q0 = t.b;
+        bool ok = ctx >= 0 && ctx <= lim;
+        if (p.cu_q != nullptr) {
+            t.q0 = __ldg(p.cu_q + t.b);
+            const int q1 = __ldg(p.cu_q + t.b + 1);
+            lq = q1 - t.q0;
+            ok = ok && t.q0 >= 0 && q1 <= p.total_q && lq >= 0 && lq <= p.max_q && lq <= ctx;
+            if (!ok) lq = 0;   // the sequence's rows are left unwritten
+        } else {
+            ctx = min(max(ctx, 0), lim);
+        }
+        if (!ok && flag && rt == 0) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
+        t.ntok = min(p.tok, lq - rt * p.tok);
+        t.q0 += rt * p.tok;
+        t.p0 = ctx - lq + rt * p.tok;
+        t.tiles = t.ntok > 0 && t.p0 >= 0
+            ? tile_range(t.p0, t.p0 + t.ntok - 1, p.window, p.sinks).count : 0;
+        t.ns = t.ntok > 0 ? max(1, (t.tiles + p.chunk - 1) / p.chunk) : 0;
+        return t;
+    };
+    // (cumulative lengths that run backwards can claim rows twice, and so more entries than
+    // the table has room for: what does not fit is dropped and flagged)
+    auto put = [&](int at, const Tile& t, int s) {
+        if (at >= p.max_entries) return;
+        p.items[2 * at] = make_int4(t.b, s | (t.ns << 16), t.q0, t.ntok);
+        p.items[2 * at + 1] = make_int4(t.p0, s * p.chunk, min(t.tiles, (s + 1) * p.chunk), 0);
+    };
+    int carry = 0;
+    const int n = p.batch * p.row_tiles;
+    for (int base = 0; base < n; base += blockDim.x) {
+        const int i = base + tid;
+        Tile t{};
+        int nfull = 0;
+        if (i < n) {
+            t = tile(i, true);
+            if (t.ns > 0) {
+                for (int k = 0; k < t.ntok; ++k) p.nsplit[t.q0 + k] = t.ns;
+                const int last = t.tiles - (t.ns - 1) * p.chunk;
+                nfull = last == p.chunk ? t.ns : t.ns - 1;
+                if (last < p.chunk) atomicAdd(s_cls + length_class(last, p.chunk), 1);
+            }
+        }
+        int block_tot = 0;
+        const int e = carry + block_exclusive_scan(nfull, warp_tot, block_tot);
+        for (int s = 0; s < nfull; ++s) put(e + s, t, s);
+        carry += block_tot;
+    }
+    __syncthreads();
+    const int cls = kLengthClasses - 1 - tid;
+    const int v = tid < kLengthClasses ? s_cls[cls] : 0;
+    int tot_short = 0;
+    const int e = block_exclusive_scan(v, warp_tot, tot_short);
+    if (tid < kLengthClasses) s_cls[cls] = carry + e;
+    __syncthreads();
+    for (int i = tid; i < n; i += blockDim.x) {
+        const Tile t = tile(i, false);
+        if (t.ns == 0) continue;
+        const int last = t.tiles - (t.ns - 1) * p.chunk;
+        if (last == p.chunk) continue;
+        put(atomicAdd(s_cls + length_class(last, p.chunk), 1), t, t.ns - 1);
+    }
+    if (tid == 0) {
+        const int total = carry + tot_short;
+        if (total > p.max_entries) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
+        p.counter[0] = 0;
+        p.counter[1] = min(total, p.max_entries) * p.hkv;
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// the worker kernel
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&a)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float max_over_keys(float v) {   // lanes with the same lane % 4
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+template <int D, bool FP8>
+struct RowStage {
+    static constexpr int ROW = FP8 ? D : 2 * D;             // bytes of a key's row
+    static constexpr int CHUNKS = ROW / 16;
+    static constexpr int KV = kTileKeys * ROW;
+    static constexpr int SCALES = 2 * KV;                   // 16 K scales, 16 V scales
+    static constexpr int META = SCALES + (FP8 ? 32 : 0);
+    static constexpr int BYTES = META + 16;
+    // byte offset of chunk c of key row r
+    __device__ static __forceinline__ int at(int r, int c) {
+        return r * ROW + ((CHUNKS >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) << 4);
+    }
+};
+
+// Ring depth: a warp keeps STAGES - 1 tiles in flight while it works on one.
+template <bool FP8>
+constexpr int row_stages() { return FP8 ? 4 : 2; }
+
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32)
+row_attention_kernel(const RowParams p) {
+    using Stage = RowStage<D, FP8>;
+    constexpr int STAGES = row_stages<FP8>();
+    constexpr int KK = D / 16;    // MMAs along D
+    constexpr int MT = D / 16;    // 16-dim tiles of O^T
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t* wsm = smem + (size_t)warp * STAGES * Stage::BYTES;
+    const uint32_t wbase = smem_u32(wsm);
+    const size_t row_bytes = (size_t)p.hkv * Stage::ROW;   // bytes between cache rows (slots)
+    const int tile_shift = p.block_shift - 4;              // 16-key tiles per block, log2
+
+    // ---------------- issue side ----------------
+    bool it_valid = false;
+    int4 it_a = make_int4(0, 0, 0, 0), it_b = it_a;
+    int it_hk = 0, it_v = 0, it_end = 0, it_plast = 0, it_blk = 0;
+    TileRange it_r{};
+    const int32_t* it_bt = nullptr;
+
+    pdl_wait();
+    const int total_items = __ldcg(p.counter + 1);
+    const int nwarps = gridDim.x * kRowWarps;
+    int nx_item = blockIdx.x * kRowWarps + warp;
+
+    auto real_tile = [&](int v) { return v < it_r.head ? v : v + it_r.skip; };
+    auto load_block = [&]() {   // the table entry of the tile to be issued next (checked there)
+        if (it_v < it_end) it_blk = __ldg(it_bt + (real_tile(it_v) >> tile_shift));
+    };
+    auto fetch = [&]() {
+        const int idx = __shfl_sync(0xffffffffu, nx_item, 0);
+        if (idx >= total_items) {
+            it_valid = false;
+            return;
+        }
+        if (lane == 0) nx_item = nwarps + atomicAdd(p.counter, 1);
+        it_valid = true;
+        const int e = idx / p.hkv;
+        it_hk = idx - e * p.hkv;
+        it_a = __ldcg(reinterpret_cast<const int4*>(p.items) + 2 * e);
+        it_b = __ldcg(reinterpret_cast<const int4*>(p.items) + 2 * e + 1);
+        it_bt = p.block_tables + (size_t)it_a.x * p.max_blocks;
+        it_plast = it_b.x + it_a.w - 1;
+        it_r = tile_range(max(it_b.x, 0), max(it_plast, 0), p.window, p.sinks);
+        it_v = it_b.y;
+        it_end = it_b.z;
+        load_block();
+    };
+    // meta: (real tile, first | last << 1, -, -); x = -1 ends the loop, x = -2 is an item
+    // without keys
+    auto issue = [&](int st) {
+        uint8_t* sb = wsm + st * Stage::BYTES;
+        int4* meta = reinterpret_cast<int4*>(sb + Stage::META);
+        if (!it_valid) {
+            if (lane == 0) *meta = make_int4(-1, 0, 0, 0);
+            cp_async_commit();
+            return;
+        }
+        const bool first = it_v == it_b.y, last = it_v + 1 >= it_end;
+        int tile = -2;
+        if (it_v < it_end) {
+            tile = real_tile(it_v);
+            const int key0 = tile * kTileKeys;
+            // keys that the item's first or any later query token sees
+            uint32_t seen = first_keys(it_plast + 1 - key0);
+            if (p.window > 0) seen &= ~first_keys(it_b.x - p.window + 1 - key0) | first_keys(p.sinks - key0);
+            int blk = it_blk;
+            if (blk < 0 || blk >= p.num_blocks) {
+                if (lane == 0) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
+                blk = 0;
+                seen = 0;   // its rows are absent
+            }
+            const int row0 = key0 & (p.block_size - 1);
+            const size_t off = ((size_t)blk * p.block_size + row0) * row_bytes + (size_t)it_hk * Stage::ROW;
+            const uint8_t* kg = static_cast<const uint8_t*>(p.k_cache) + off;
+            const uint8_t* vg = static_cast<const uint8_t*>(p.v_cache) + off;
+#pragma unroll
+            for (int i = 0; i < Stage::CHUNKS / 2; ++i) {
+                const int idx = lane + 32 * i;
+                const int r = idx / Stage::CHUNKS, c = idx % Stage::CHUNKS;
+                const int nb = (seen >> r) & 1 ? 16 : 0;
+                cp_async16(sb + Stage::at(r, c), kg + (size_t)r * row_bytes + c * 16, nb);
+                cp_async16(sb + Stage::KV + Stage::at(r, c), vg + (size_t)r * row_bytes + c * 16, nb);
+            }
+            if constexpr (FP8) {
+                if (lane < 2) {
+                    const size_t so = ((size_t)blk * p.hkv + it_hk) * p.block_size + row0;
+                    cp_async16(sb + Stage::SCALES + lane * 16, (lane ? p.v_scales : p.k_scales) + so, 16);
+                }
+            }
+            if (lane == 0) *meta = make_int4(tile, (first ? 1 : 0) | (last ? 2 : 0), (int)seen, 0);
+        } else if (lane == 0) {
+            *meta = make_int4(-2, 3, 0, 0);
+        }
+        cp_async_commit();
+        ++it_v;
+        if (last) fetch(); else load_block();
+    };
+
+    // ---------------- consume side ----------------
+    int4 a = make_int4(0, 0, 0, 0), b = a;
+    int hk = 0;                    // item being consumed
+    uint32_t qf[NT][KK][2];
+    float qs[NT][2];               // score factor of rows 8 j + 2 t + {0, 1}
+    int pos[NT][2];                // their positions (-1: no such row)
+    float o[NT][MT][4];
+    float m[NT][2], mv[NT][2], l[NT][2];
+    (void)mv;
+
+    auto start = [&](const int4& na, const int4& nb, int nhk) {
+        a = na;
+        b = nb;
+        hk = nhk;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            // Q^T fragment: row n = 8 j + g, the dims that this lane's K chunks hold
+            const int n = 8 * j + g;
+            const int tk = n / p.group, hd = n - tk * p.group;
+            const bool ok = tk < a.w;
+            const uint16_t* src = p.q + ((size_t)(a.z + (ok ? tk : 0)) * p.hq + hk * p.group + hd) * D;
+            float fac = p.scale_log2;
+            if constexpr (FP8) {
+                uint32_t w[KK][2];
+#pragma unroll
+                for (int i = 0; i < KK / 4; ++i) {   // 16 dims per 16-byte chunk of codes
+                    const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(src + ((KK / 4) * t + i) * 16)) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(src + ((KK / 4) * t + i) * 16) + 1) : make_uint4(0, 0, 0, 0);
+                    w[4 * i][0] = u.x; w[4 * i][1] = u.y; w[4 * i + 1][0] = u.z; w[4 * i + 1][1] = u.w;
+                    w[4 * i + 2][0] = v.x; w[4 * i + 2][1] = v.y; w[4 * i + 3][0] = v.z; w[4 * i + 3][1] = v.w;
+                }
+                uint32_t mx = 0;
+#pragma unroll
+                for (int i = 0; i < KK; ++i) mx = __vmaxu2(mx, __vmaxu2(w[i][0] & 0x7fff7fffu, w[i][1] & 0x7fff7fffu));
+                mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                // 2^-eq brings the row into (-2, 2); rows too small or not finite stay in range
+                const int eq = min(max((int)(mx >> 7), 1), 253);
+                const float inv = scale_value(254 - eq);
+                fac *= scale_value(eq);
+#pragma unroll
+                for (int i = 0; i < KK; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) qf[j][i][x] = pack_half2(bf16_lo(w[i][x]) * inv, bf16_hi(w[i][x]) * inv);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KK / 2; ++i) {   // 8 dims per chunk
+                    const int c = 2 * t + (i & 1) + 8 * (i >> 1);
+                    const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(src + c * 8)) : make_uint4(0, 0, 0, 0);
+                    qf[j][2 * i][0] = u.x; qf[j][2 * i][1] = u.y; qf[j][2 * i + 1][0] = u.z; qf[j][2 * i + 1][1] = u.w;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                qs[j][x] = __shfl_sync(0xffffffffu, fac, (2 * t + x) * 4);
+                const int r = 8 * j + 2 * t + x, rt = r / p.group;
+                pos[j][x] = rt < a.w ? b.x + rt : -1;
+                m[j][x] = mv[j][x] = -INFINITY;
+                l[j][x] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[j][i][x] = 0.f;
+        }
+    };
+
+    auto epilogue = [&]() {
+        const int s = a.y & 0xffff, ns = a.y >> 16;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float sum = l[j][x];
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                const int r = 8 * j + 2 * t + x, tk = r / p.group;
+                if (tk >= a.w) continue;
+                const size_t row = (size_t)(a.z + tk) * p.hq + hk * p.group + (r - tk * p.group);
+                float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                if constexpr (FP8) inv = sum == 0.f ? 0.f : inv * exp2f(mv[j][x] - m[j][x]);
+                const float lse = sum == 0.f ? -INFINITY : (m[j][x] + log2f(sum)) * kLn2;
+                if (g == 0) {
+                    if (ns > 1) __stcg(p.lse_part + row * p.s_max + s, lse);
+                    else if (p.lse_out != nullptr) p.lse_out[row] = lse;
+                }
+                if constexpr (FP8) {
+                    // this lane's dims: g * (D / 8) .. + D / 8
+                    constexpr int N = D / 8;
+                    float v[N];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        v[2 * i] = o[j][i][x] * inv;
+                        v[2 * i + 1] = o[j][i][2 + x] * inv;
+                    }
+                    if (ns > 1) {
+                        float* dst = p.o_part + (row * p.s_max + s) * D + g * N;
+#pragma unroll
+                        for (int i = 0; i < N; i += 4)
+                            __stcg(reinterpret_cast<float4*>(dst + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                    } else {
+                        uint16_t* dst = p.out + row * D + g * N;
+#pragma unroll
+                        for (int i = 0; i < N; i += 8)
+                            *reinterpret_cast<uint4*>(dst + i) =
+                                make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                                           pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float v = o[j][i][2 * y + x] * inv;
+                            const int dim = 16 * i + 8 * y + g;
+                            if (ns > 1) __stcg(p.o_part + (row * p.s_max + s) * D + dim, v);
+                            else reinterpret_cast<__nv_bfloat16*>(p.out)[row * D + dim] = __float2bfloat16_rn(v);
+                        }
+                }
+            }
+    };
+
+    auto consume = [&](int st, const int4& meta) {
+        const uint8_t* sb = wsm + st * Stage::BYTES;
+        const uint32_t sa = wbase + st * Stage::BYTES;
+        const int key0 = meta.x * kTileKeys;
+        // ---- S^T = K Q^T ----
+        float sc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < KK / 4; ++i) {
+                const int c = (KK / 4) * t + i;
+                const uint4 u = *reinterpret_cast<const uint4*>(sb + Stage::at(g, c));
+                const uint4 v = *reinterpret_cast<const uint4*>(sb + Stage::at(g + 8, c));
+                const uint32_t lo[4] = {u.x, u.y, u.z, u.w}, hi[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    uint32_t f[4];
+                    e4m3x4_to_half2(lo[y], f[0], f[2]);
+                    e4m3x4_to_half2(hi[y], f[1], f[3]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mma_f16(sc[j], f, qf[j][4 * i + y][0], qf[j][4 * i + y][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < KK / 2; ++i) {
+                const int c = 2 * t + (i & 1) + 8 * (i >> 1);
+                const uint4 u = *reinterpret_cast<const uint4*>(sb + Stage::at(g, c));
+                const uint4 v = *reinterpret_cast<const uint4*>(sb + Stage::at(g + 8, c));
+                const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma_bf16(sc[j], f0, qf[j][2 * i][0], qf[j][2 * i][1]);
+                    mma_bf16(sc[j], f1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+                }
+            }
+        }
+        // ---- softmax: this lane has keys g (x = 0, 1) and g + 8 (x = 2, 3) of rows 2t, 2t + 1 ----
+        float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f};
+        if constexpr (FP8) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                kf[y] = scale_value(sb[Stage::SCALES + g + 8 * y]);
+                ve[y] = (float)((int)sb[Stage::SCALES + 16 + g + 8 * y] - 127);
+            }
+        }
+        // a tile that every row sees whole needs no mask (rows that do not exist may see it)
+        const bool open = meta.z == 0xffff && key0 + kTileKeys - 1 <= b.x &&
+                          (p.window == 0 || key0 > b.x + a.w - 1 - p.window || key0 + kTileKeys <= p.sinks);
+        bool over = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[j][x] *= qs[j][x & 1] * kf[x >> 1];
+            if (!open) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t seen = seen_keys(key0, pos[j][x], p.window, p.sinks) & (uint32_t)meta.z;
+                    if (!((seen >> g) & 1)) sc[j][x] = -INFINITY;
+                    if (!((seen >> (g + 8)) & 1)) sc[j][2 + x] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                over |= sc[j][x] > m[j][x & 1] + kRescaleSlack;
+                if constexpr (FP8) over |= sc[j][x] + ve[x >> 1] > mv[j][x & 1] + kRescaleSlack;
+            }
+        }
+        // lazy rescaling, as in attn_warp.cuh: the references move only when some score is
+        // more than 2^8 above them
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float mn = fmaxf(m[j][x], max_over_keys(fmaxf(sc[j][x], sc[j][2 + x])));
+                    const float al = mn > m[j][x] ? fast_exp2(m[j][x] - mn) : 1.f;
+                    l[j][x] *= al;
+                    m[j][x] = mn;
+                    float ao = al;
+                    if constexpr (FP8) {
+                        const float vn = fmaxf(mv[j][x], max_over_keys(fmaxf(sc[j][x] + ve[0], sc[j][2 + x] + ve[1])));
+                        ao = vn > mv[j][x] ? fast_exp2(mv[j][x] - vn) : 1.f;
+                        mv[j][x] = vn;
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        o[j][i][x] *= ao;
+                        o[j][i][2 + x] *= ao;
+                    }
+                }
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+        (void)pl;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                // a masked score (-inf) weighs 0 also when the row has seen no key yet
+                const bool hide = sc[j][x] == -INFINITY;
+                const float e = hide ? 0.f : fast_exp2(sc[j][x] - m[j][x & 1]);
+                l[j][x & 1] += e;
+                w[x] = e;
+                if constexpr (FP8) w[x] = hide ? 0.f : fast_exp2(sc[j][x] + ve[x >> 1] - mv[j][x & 1]);
+            }
+            if constexpr (FP8) {
+                ph[j][0] = transpose8x8(pack_half2(w[0], w[1]));
+                ph[j][1] = transpose8x8(pack_half2(w[2], w[3]));
+            } else {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t h = pack_bf16x2(w[2 * y], w[2 * y + 1]);
+                    ph[j][y] = transpose8x8(h);
+                    pl[j][y] = transpose8x8(pack_bf16x2(w[2 * y] - bf16_lo(h), w[2 * y + 1] - bf16_hi(h)));
+                }
+            }
+        }
+        // ---- O^T += V^T P^T ----
+        const uint8_t* vs = sb + Stage::KV;
+        if constexpr (FP8) {
+            constexpr int N = D / 8;   // dims of this lane: g * N ..
+            uint32_t v[4][N / 4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = 2 * t + (y & 1) + 8 * (y >> 1);
+                if constexpr (N == 16) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(vs + Stage::at(r, g));
+                    v[y][0] = u.x; v[y][1] = u.y; v[y][2] = u.z; v[y][3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(vs + Stage::at(r, g >> 1) + (g & 1) * 8);
+                    v[y][0] = u.x; v[y][1] = u.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                // dims 2 i, 2 i + 1 of the four keys: (key 2t, key 2t + 1) pairs, then 2t + 8, 2t + 9
+                const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+                uint32_t f[4];
+                e4m3x4_to_half2(__byte_perm(v[0][i / 2], v[1][i / 2], sel), f[0], f[1]);
+                e4m3x4_to_half2(__byte_perm(v[2][i / 2], v[3][i / 2], sel), f[2], f[3]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma_f16(o[j][i], f, ph[j][0], ph[j][1]);
+            }
+        } else {
+            const int r = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                uint32_t f[4];
+                ldmatrix4_trans(f, sa + Stage::KV + Stage::at(r, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma_bf16(o[j][i], f, ph[j][0], ph[j][1]);
+                    mma_bf16(o[j][i], f, pl[j][0], pl[j][1]);
+                }
+            }
+        }
+    };
+
+    // The descriptions of items that are in the ring but not started yet wait in shared memory
+    // beside it: at most STAGES of them, one per stage.
+    int4* queue = reinterpret_cast<int4*>(smem + (size_t)kRowWarps * STAGES * Stage::BYTES) + warp * STAGES * 3;
+    int q_in = 0, q_out = 0;
+    auto push = [&]() {   // the item that fetch() just took
+        if (it_valid && lane == 0) {
+            queue[3 * q_in] = it_a;
+            queue[3 * q_in + 1] = it_b;
+            queue[3 * q_in + 2] = make_int4(it_hk, 0, 0, 0);
+        }
+        q_in = q_in + 1 == STAGES ? 0 : q_in + 1;
+    };
+
+    fetch();
+    int cs = 0, is = 0;
+    auto step_issue = [&]() {
+        if (it_valid && it_v == it_b.y) push();
+        issue(is);
+        is = is + 1 == STAGES ? 0 : is + 1;
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) step_issue();
+    while (true) {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();
+        step_issue();
+        const int4 meta = *reinterpret_cast<const int4*>(wsm + cs * Stage::BYTES + Stage::META);
+        if (meta.x == -1) break;
+        if (meta.y & 1) {
+            start(queue[3 * q_out], queue[3 * q_out + 1], queue[3 * q_out + 2].x);
+            q_out = q_out + 1 == STAGES ? 0 : q_out + 1;
+        }
+        if (meta.x >= 0) consume(cs, meta);
+        if (meta.y & 2) epilogue();
+        cs = cs + 1 == STAGES ? 0 : cs + 1;
+    }
+    cp_async_wait<0>();
+    pdl_launch_dependents();
+}
+
+// ------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------
+template <int D, bool FP8>
+constexpr int row_smem() {
+    return kRowWarps * row_stages<FP8>() * (RowStage<D, FP8>::BYTES + 48);
+}
+
+template <int D, bool FP8, int NT>
+cudaError_t launch_rows(const RowParams& p, long long max_items, cudaStream_t stream) {
+    static std::once_flag once[64];
+    static int per_sm[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    dev &= 63;
+    auto kern = row_attention_kernel<D, FP8, NT>;
+    constexpr int smem = row_smem<D, FP8>();
+    std::call_once(once[dev], [&] {
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kRowWarps * 32, smem) != cudaSuccess) n = 1;
+        per_sm[dev] = std::max(1, n);
+    });
+    const long long want = (max_items + kRowWarps - 1) / kRowWarps;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::max(1LL, std::min<long long>((long long)device_sm_count() * per_sm[dev], want)));
+    cfg.blockDim = dim3(kRowWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+struct RowGeometry {
+    int tok, row_tiles, nt, chunk, s_max;
+    long long tiles;     // bound on (sequence, row tile) pairs
+    size_t counter, nsplit, items, lse_part, o_part, total;
+};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+RowGeometry row_geometry(int batch, int total_q, int max_q, int hq, int hkv, int head_dim, int max_ctx,
+                         int block_size, int window, int sinks, int num_splits) {
+    RowGeometry r{};
+    const int group = std::max(1, hq / hkv);
+    r.nt = max_q * group <= 8 ? 1 : 2;
+    r.tok = std::max(1, std::min(max_q, 8 * r.nt / group));
+    r.row_tiles = std::max(1, (max_q + r.tok - 1) / r.tok);
+    r.tiles = std::min((long long)batch * r.row_tiles, (long long)batch + total_q / r.tok);
+    // 16-key tiles that a row tile can see
+    long long seen = ((long long)std::max(0, max_ctx) + kTileKeys - 1) / kTileKeys;
+    if (window > 0)
+        seen = std::min(seen, ((long long)window + r.tok + kTileKeys - 2) / kTileKeys + 1 +
+                                  ((long long)sinks + kTileKeys - 1) / kTileKeys);
+    seen = std::max(1LL, seen);
+    const int eff = (int)std::min<long long>(seen * kTileKeys, 0x7ffffff0);
+    const int per = decode_chunk_keys((int)std::min<long long>(r.tiles, 0x7fffffff), hkv, eff, block_size, num_splits);
+    r.chunk = per / kTileKeys;
+    // the partition index travels in 15 bits
+    r.chunk = (int)std::max<long long>(r.chunk, (seen + 32766) / 32767);
+    r.s_max = (int)((seen + r.chunk - 1) / r.chunk);
+    size_t off = 256;
+    r.counter = 0;
+    r.nsplit = off; off = align256(off + sizeof(int32_t) * (size_t)total_q);
+    r.items = off; off = align256(off + 2 * sizeof(int4) * (size_t)r.tiles * r.s_max);
+    r.lse_part = off; off = align256(off + (r.s_max > 1 ? sizeof(float) * (size_t)total_q * hq * r.s_max : 0));
+    r.o_part = off; off = align256(off + (r.s_max > 1 ? sizeof(float) * (size_t)total_q * hq * r.s_max * head_dim : 0));
+    r.total = off;
+    return r;
+}
+
+}  // namespace
+
+size_t row_attention_workspace_bytes(int batch, int total_q, int max_q, int hq, int hkv, int head_dim,
+                                     int max_ctx, int block_size, int window, int sinks, int num_splits) {
+    return row_geometry(batch, total_q, max_q, hq, hkv, head_dim, max_ctx, block_size, window, sinks, num_splits).total;
+}
+
+nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
+    const RowGeometry r = row_geometry(c.batch, c.total_q, c.max_seqlen_q, c.hq, c.hkv, c.head_dim,
+                                       c.max_context_len, c.block_size, c.window, c.num_sinks, c.num_splits);
+    if (c.workspace_bytes < r.total) {
+        set_error("workspace too small: %zu bytes given, %zu needed", c.workspace_bytes, r.total);
+        return NVPA_ERR_WORKSPACE_TOO_SMALL;
+    }
+    if (r.tiles * r.s_max * c.hkv > 0x7fffffffLL / 2 || (long long)c.batch * r.row_tiles > 0x7fffffffLL / 2) {
+        set_error("more than 2^30 work items");
+        return NVPA_ERR_UNSUPPORTED;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+    RowParams p{};
+    p.q = static_cast<const uint16_t*>(c.q);
+    p.k_cache = c.k_cache;
+    p.v_cache = c.v_cache;
+    p.k_scales = c.k_scales;
+    p.v_scales = c.v_scales;
+    p.block_tables = c.block_tables;
+    p.context_lens = c.context_lens;
+    p.cu_q = c.cu_seqlens_q;
+    p.out = static_cast<uint16_t*>(c.out);
+    p.lse_out = c.lse_out;
+    p.counter = reinterpret_cast<int32_t*>(ws + r.counter);
+    p.nsplit = reinterpret_cast<int32_t*>(ws + r.nsplit);
+    p.items = reinterpret_cast<int4*>(ws + r.items);
+    p.lse_part = reinterpret_cast<float*>(ws + r.lse_part);
+    p.o_part = reinterpret_cast<float*>(ws + r.o_part);
+    p.err = c.err_flag;
+    p.batch = c.batch;
+    p.total_q = c.total_q;
+    p.max_q = c.max_seqlen_q;
+    p.hq = c.hq;
+    p.hkv = c.hkv;
+    p.group = c.hq / c.hkv;
+    p.max_blocks = c.max_blocks_per_seq;
+    p.num_blocks = c.num_blocks;
+    p.block_size = c.block_size;
+    p.block_shift = __builtin_ctz((unsigned)c.block_size);
+    p.max_ctx = c.max_context_len;
+    // (a window as long as the longest context hides nothing)
+    p.window = c.window >= c.max_context_len ? 0 : c.window;
+    p.sinks = std::min(c.num_sinks, c.max_context_len);
+    p.max_entries = (int)(r.tiles * r.s_max);
+    p.tok = r.tok;
+    p.row_tiles = r.row_tiles;
+    p.chunk = r.chunk;
+    p.s_max = r.s_max;
+    p.scale_log2 = c.scale * kLog2e;
+    row_plan_kernel<<<1, 1024, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_failure(e, "row attention plan launch");
+    count_launches(1);
+    const long long max_items = r.tiles * r.s_max * c.hkv;
+    const bool fp8 = c.k_scales != nullptr;
+    e = cudaErrorInvalidValue;
+#define NVPA_CASE(DD, FF, NN) \
+    if (c.head_dim == DD && fp8 == FF && r.nt == NN) e = launch_rows<DD, FF, NN>(p, max_items, stream);
+    NVPA_CASE(128, false, 1) NVPA_CASE(128, false, 2) NVPA_CASE(128, true, 1) NVPA_CASE(128, true, 2)
+    NVPA_CASE(64, false, 1) NVPA_CASE(64, false, 2) NVPA_CASE(64, true, 1) NVPA_CASE(64, true, 2)
+#undef NVPA_CASE
+    if (e != cudaSuccess) return cuda_failure(e, "row attention launch");
+    if (r.s_max > 1) {
+        AttnParams cp{};
+        cp.out = p.out;
+        cp.lse_out = p.lse_out;
+        cp.o_part = p.o_part;
+        cp.lse_part = p.lse_part;
+        cp.nsplit = p.nsplit;
+        cp.batch = c.total_q;
+        cp.hq = c.hq;
+        cp.s_max = r.s_max;
+        e = launch_decode_combine(cp, c.head_dim, stream);
+        if (e != cudaSuccess) return cuda_failure(e, "row attention combine launch");
+        count_launches(1);
+    }
+    return NVPA_OK;
+}
+
+}  // namespace nvpa
