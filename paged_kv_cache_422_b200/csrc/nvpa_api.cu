@@ -473,14 +473,25 @@ nvpa_status_t nvpa_paged_decode_attention_window(
     return st != NVPA_OK || empty ? st : run_row_attention(c, stream);
 }
 
+// Which kernel a chunk call takes: up to kRowKernelRows query rows per KV head (tokens times
+// heads of its group) go to the row kernel, which reads the keys once for 16 rows; more go to
+// the 128-row tiles.
+constexpr int kRowKernelRows = 16;
+static bool chunk_on_tiles(int max_seqlen_q, int num_q_heads, int num_kv_heads) {
+    return (long long)max_seqlen_q * (num_q_heads / num_kv_heads) > kRowKernelRows;
+}
+
 size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
                                            int head_dim, int max_seqlen_q, int max_context_len, int block_size,
                                            int window, int num_sinks, int num_splits) {
     if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || !attn_block_size_ok(block_size) ||
         !window_sizes_ok(num_q_heads, num_kv_heads, head_dim, max_context_len, window, num_sinks, num_splits))
         return 0;
-    return row_attention_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
-                                         max_context_len, block_size, window, num_sinks, num_splits);
+    return chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads)
+               ? chunk_tiles_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
+                                             max_context_len, window, num_sinks, num_splits)
+               : row_attention_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
+                                               max_context_len, block_size, window, num_sinks, num_splits);
 }
 
 nvpa_status_t nvpa_chunk_attention(
@@ -499,7 +510,8 @@ nvpa_status_t nvpa_chunk_attention(
     const nvpa_status_t st = check_window_call(c, cache_type, &empty);
     if (st != NVPA_OK || empty) return st;
     NVPA_REQUIRE(cu_seqlens_q != nullptr, NVPA_ERR_INVALID_ARG, "null pointer");
-    return run_row_attention(c, stream);
+    return chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads) ? run_chunk_tiles(c, stream)
+                                                                   : run_row_attention(c, stream);
 }
 
 nvpa_status_t nvpa_check_bounded_wait(int32_t* err_flag, cudaStream_t stream) {

@@ -95,6 +95,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
            "r"(smem_u32(bar))
         : "memory");
 }
+// Untiled copy into shared memory, completing `bytes` on `bar`: both addresses 16-byte
+// aligned, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
 // Generic-proxy writes to shared memory made visible to the async proxy (TMA, tcgen05).
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
