@@ -230,13 +230,15 @@ __device__ __forceinline__ float max_over_keys(float v) {   // lanes with the sa
     return v;
 }
 
+// A stage of a warp's ring: TILES 16-key tiles that are worked on together.
 template <int D, bool FP8>
 struct RowStage {
+    static constexpr int TILES = FP8 ? 2 : 1;
     static constexpr int ROW = FP8 ? D : 2 * D;             // bytes of a key's row
     static constexpr int CHUNKS = ROW / 16;
-    static constexpr int KV = kTileKeys * ROW;
-    static constexpr int SCALES = 2 * KV;                   // 16 K scales, 16 V scales
-    static constexpr int META = SCALES + (FP8 ? 32 : 0);
+    static constexpr int KV = kTileKeys * ROW;              // K of a tile, then its V
+    static constexpr int SCALES = TILES * 2 * KV;           // per tile 16 K scales, 16 V scales
+    static constexpr int META = SCALES + (FP8 ? TILES * 32 : 0);
     static constexpr int BYTES = META + 16;
     // byte offset of chunk c of key row r
     __device__ static __forceinline__ int at(int r, int c) {
@@ -244,15 +246,16 @@ struct RowStage {
     }
 };
 
-// Ring depth: a warp keeps STAGES - 1 tiles in flight while it works on one.
-template <bool FP8>
-constexpr int row_stages() { return FP8 ? 4 : 2; }
+// Ring depth: a warp loads one stage while it works on the other.
+constexpr int kRowStages = 2;
 
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32)
 row_attention_kernel(const RowParams p) {
     using Stage = RowStage<D, FP8>;
-    constexpr int STAGES = row_stages<FP8>();
+    constexpr int STAGES = kRowStages;
+    constexpr int TILES = Stage::TILES;
+    constexpr uint32_t ALL = TILES == 2 ? 0xffffffffu : 0xffffu;   // every key of a stage
     constexpr int KK = D / 16;    // MMAs along D
     constexpr int MT = D / 16;    // 16-dim tiles of O^T
     extern __shared__ __align__(128) uint8_t smem[];
@@ -266,7 +269,8 @@ row_attention_kernel(const RowParams p) {
     // ---------------- issue side ----------------
     bool it_valid = false;
     int4 it_a = make_int4(0, 0, 0, 0), it_b = it_a;
-    int it_hk = 0, it_v = 0, it_end = 0, it_plast = 0, it_blk = 0;
+    int it_hk = 0, it_v = 0, it_end = 0, it_plast = 0;
+    int it_blk[TILES];
     TileRange it_r{};
     const int32_t* it_bt = nullptr;
 
@@ -276,8 +280,10 @@ row_attention_kernel(const RowParams p) {
     int nx_item = blockIdx.x * kRowWarps + warp;
 
     auto real_tile = [&](int v) { return v < it_r.head ? v : v + it_r.skip; };
-    auto load_block = [&]() {   // the table entry of the tile to be issued next (checked there)
-        if (it_v < it_end) it_blk = __ldg(it_bt + (real_tile(it_v) >> tile_shift));
+    auto load_block = [&]() {   // the table entries of the stage to be issued next (checked there)
+#pragma unroll
+        for (int u = 0; u < TILES; ++u)
+            if (it_v + u < it_end) it_blk[u] = __ldg(it_bt + (real_tile(it_v + u) >> tile_shift));
     };
     auto fetch = [&]() {
         const int idx = __shfl_sync(0xffffffffu, nx_item, 0);
@@ -298,8 +304,11 @@ row_attention_kernel(const RowParams p) {
         it_end = it_b.z;
         load_block();
     };
-    // meta: (real tile, first | last << 1, -, -); x = -1 ends the loop, x = -2 is an item
-    // without keys
+    // this lane's chunk of rows lane / CHUNKS + i * (32 / CHUNKS)
+    const size_t lane_off = (size_t)(lane / Stage::CHUNKS) * row_bytes + (lane % Stage::CHUNKS) * 16;
+    const size_t row_step = (size_t)(32 / Stage::CHUNKS) * row_bytes;
+    // meta: (real tile, first | last << 1, seen keys, real second tile); tile -1 ends the loop,
+    // -2 is an item without keys
     auto issue = [&](int st) {
         uint8_t* sb = wsm + st * Stage::BYTES;
         int4* meta = reinterpret_cast<int4*>(sb + Stage::META);
@@ -308,44 +317,55 @@ row_attention_kernel(const RowParams p) {
             cp_async_commit();
             return;
         }
-        const bool first = it_v == it_b.y, last = it_v + 1 >= it_end;
-        int tile = -2;
+        const bool first = it_v == it_b.y, last = it_v + TILES >= it_end;
         if (it_v < it_end) {
-            tile = real_tile(it_v);
-            const int key0 = tile * kTileKeys;
-            // keys that the item's first or any later query token sees
-            uint32_t seen = first_keys(it_plast + 1 - key0);
-            if (p.window > 0) seen &= ~first_keys(it_b.x - p.window + 1 - key0) | first_keys(p.sinks - key0);
-            int blk = it_blk;
-            if (blk < 0 || blk >= p.num_blocks) {
-                if (lane == 0) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
-                blk = 0;
-                seen = 0;   // its rows are absent
-            }
-            const int row0 = key0 & (p.block_size - 1);
-            const size_t off = ((size_t)blk * p.block_size + row0) * row_bytes + (size_t)it_hk * Stage::ROW;
-            const uint8_t* kg = static_cast<const uint8_t*>(p.k_cache) + off;
-            const uint8_t* vg = static_cast<const uint8_t*>(p.v_cache) + off;
+            int tile[2] = {0, 0};
+            uint32_t all_seen = 0;
 #pragma unroll
-            for (int i = 0; i < Stage::CHUNKS / 2; ++i) {
-                const int idx = lane + 32 * i;
-                const int r = idx / Stage::CHUNKS, c = idx % Stage::CHUNKS;
-                const int nb = (seen >> r) & 1 ? 16 : 0;
-                cp_async16(sb + Stage::at(r, c), kg + (size_t)r * row_bytes + c * 16, nb);
-                cp_async16(sb + Stage::KV + Stage::at(r, c), vg + (size_t)r * row_bytes + c * 16, nb);
-            }
-            if constexpr (FP8) {
-                if (lane < 2) {
-                    const size_t so = ((size_t)blk * p.hkv + it_hk) * p.block_size + row0;
-                    cp_async16(sb + Stage::SCALES + lane * 16, (lane ? p.v_scales : p.k_scales) + so, 16);
+            for (int u = 0; u < TILES; ++u) {
+                const bool have = it_v + u < it_end;
+                tile[u] = real_tile(it_v + (have ? u : 0));
+                const int key0 = tile[u] * kTileKeys;
+                // keys that the item's first or any later query token sees
+                uint32_t seen = have ? first_keys(it_plast + 1 - key0) : 0;
+                if (p.window > 0) seen &= ~first_keys(it_b.x - p.window + 1 - key0) | first_keys(p.sinks - key0);
+                int blk = have ? it_blk[u] : it_blk[0];
+                if (blk < 0 || blk >= p.num_blocks) {
+                    if (lane == 0) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
+                    blk = 0;
+                    seen = 0;   // its rows are absent
                 }
+                const int row0 = key0 & (p.block_size - 1);
+                const size_t off = ((size_t)blk * p.block_size + row0) * row_bytes + (size_t)it_hk * Stage::ROW + lane_off;
+                const uint8_t* kg = static_cast<const uint8_t*>(p.k_cache) + off;
+                const uint8_t* vg = static_cast<const uint8_t*>(p.v_cache) + off;
+                uint8_t* kd = sb + u * 2 * Stage::KV;
+                auto copy = [&](bool whole) {
+#pragma unroll
+                    for (int i = 0; i < Stage::CHUNKS / 2; ++i) {
+                        const int r = lane / Stage::CHUNKS + i * (32 / Stage::CHUNKS);
+                        const int nb = whole || ((seen >> r) & 1) ? 16 : 0;   // 0: zero-filled, not read
+                        const int at = Stage::at(r, lane % Stage::CHUNKS);
+                        cp_async16(kd + at, kg + i * row_step, nb);
+                        cp_async16(kd + Stage::KV + at, vg + i * row_step, nb);
+                    }
+                };
+                if (seen == 0xffffu) copy(true);
+                else copy(false);
+                if constexpr (FP8) {
+                    if (lane < 2) {
+                        const size_t so = ((size_t)blk * p.hkv + it_hk) * p.block_size + row0;
+                        cp_async16(sb + Stage::SCALES + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + so, 16);
+                    }
+                }
+                all_seen |= seen << (16 * u);
             }
-            if (lane == 0) *meta = make_int4(tile, (first ? 1 : 0) | (last ? 2 : 0), (int)seen, 0);
+            if (lane == 0) *meta = make_int4(tile[0], (first ? 1 : 0) | (last ? 2 : 0), (int)all_seen, tile[1]);
         } else if (lane == 0) {
             *meta = make_int4(-2, 3, 0, 0);
         }
         cp_async_commit();
-        ++it_v;
+        it_v += TILES;
         if (last) fetch(); else load_block();
     };
 
@@ -475,73 +495,93 @@ row_attention_kernel(const RowParams p) {
     auto consume = [&](int st, const int4& meta) {
         const uint8_t* sb = wsm + st * Stage::BYTES;
         const uint32_t sa = wbase + st * Stage::BYTES;
-        const int key0 = meta.x * kTileKeys;
+        const int key0[2] = {meta.x * kTileKeys, meta.w * kTileKeys};
         // ---- S^T = K Q^T ----
-        float sc[NT][4];
+        float sc[TILES][NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int u = 0; u < TILES; ++u)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[u][j][x] = 0.f;
         if constexpr (FP8) {
 #pragma unroll
             for (int i = 0; i < KK / 4; ++i) {
                 const int c = (KK / 4) * t + i;
-                const uint4 u = *reinterpret_cast<const uint4*>(sb + Stage::at(g, c));
-                const uint4 v = *reinterpret_cast<const uint4*>(sb + Stage::at(g + 8, c));
-                const uint32_t lo[4] = {u.x, u.y, u.z, u.w}, hi[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint32_t f[4];
-                    e4m3x4_to_half2(lo[y], f[0], f[2]);
-                    e4m3x4_to_half2(hi[y], f[1], f[3]);
+                for (int u = 0; u < TILES; ++u) {
+                    const uint8_t* ks = sb + u * 2 * Stage::KV;
+                    const uint4 a0 = *reinterpret_cast<const uint4*>(ks + Stage::at(g, c));
+                    const uint4 a1 = *reinterpret_cast<const uint4*>(ks + Stage::at(g + 8, c));
+                    const uint32_t lo[4] = {a0.x, a0.y, a0.z, a0.w}, hi[4] = {a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) mma_f16(sc[j], f, qf[j][4 * i + y][0], qf[j][4 * i + y][1]);
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t f[4];
+                        e4m3x4_to_half2(lo[y], f[0], f[2]);
+                        e4m3x4_to_half2(hi[y], f[1], f[3]);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) mma_f16(sc[u][j], f, qf[j][4 * i + y][0], qf[j][4 * i + y][1]);
+                    }
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < KK / 2; ++i) {
                 const int c = 2 * t + (i & 1) + 8 * (i >> 1);
-                const uint4 u = *reinterpret_cast<const uint4*>(sb + Stage::at(g, c));
-                const uint4 v = *reinterpret_cast<const uint4*>(sb + Stage::at(g + 8, c));
-                const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
+                const uint4 a0 = *reinterpret_cast<const uint4*>(sb + Stage::at(g, c));
+                const uint4 a1 = *reinterpret_cast<const uint4*>(sb + Stage::at(g + 8, c));
+                const uint32_t f0[4] = {a0.x, a1.x, a0.y, a1.y}, f1[4] = {a0.z, a1.z, a0.w, a1.w};
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    mma_bf16(sc[j], f0, qf[j][2 * i][0], qf[j][2 * i][1]);
-                    mma_bf16(sc[j], f1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+                    mma_bf16(sc[0][j], f0, qf[j][2 * i][0], qf[j][2 * i][1]);
+                    mma_bf16(sc[0][j], f1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
                 }
             }
         }
         // ---- softmax: this lane has keys g (x = 0, 1) and g + 8 (x = 2, 3) of rows 2t, 2t + 1 ----
-        float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f};
-        if constexpr (FP8) {
+        float kf[TILES][2], ve[TILES][2];
+#pragma unroll
+        for (int u = 0; u < TILES; ++u)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                kf[y] = scale_value(sb[Stage::SCALES + g + 8 * y]);
-                ve[y] = (float)((int)sb[Stage::SCALES + 16 + g + 8 * y] - 127);
+                kf[u][y] = 1.f;
+                ve[u][y] = 0.f;
+                if constexpr (FP8) {
+                    const uint8_t* ss = sb + Stage::SCALES + u * 32 + g + 8 * y;
+                    kf[u][y] = scale_value(ss[0]);
+                    ve[u][y] = (float)((int)ss[16] - 127);
+                }
             }
-        }
-        // a tile that every row sees whole needs no mask (rows that do not exist may see it)
-        const bool open = meta.z == 0xffff && key0 + kTileKeys - 1 <= b.x &&
-                          (p.window == 0 || key0 > b.x + a.w - 1 - p.window || key0 + kTileKeys <= p.sinks);
+        // tiles that every row sees whole need no mask (rows that do not exist may see them)
+        bool open = (uint32_t)meta.z == ALL;
+#pragma unroll
+        for (int u = 0; u < TILES; ++u)
+            open = open && key0[u] + kTileKeys - 1 <= b.x &&
+                   (p.window == 0 || key0[u] > b.x + a.w - 1 - p.window || key0[u] + kTileKeys <= p.sinks);
         bool over = false;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sc[j][x] *= qs[j][x & 1] * kf[x >> 1];
+            for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[u][j][x] *= FP8 ? qs[j][x & 1] * kf[u][x >> 1] : qs[j][x & 1];
             if (!open) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t seen = seen_keys(key0, pos[j][x], p.window, p.sinks) & (uint32_t)meta.z;
-                    if (!((seen >> g) & 1)) sc[j][x] = -INFINITY;
-                    if (!((seen >> (g + 8)) & 1)) sc[j][2 + x] = -INFINITY;
-                }
+                for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t seen = seen_keys(key0[u], pos[j][x], p.window, p.sinks) & ((uint32_t)meta.z >> (16 * u));
+                        if (!((seen >> g) & 1)) sc[u][j][x] = -INFINITY;
+                        if (!((seen >> (g + 8)) & 1)) sc[u][j][2 + x] = -INFINITY;
+                    }
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                over |= sc[j][x] > m[j][x & 1] + kRescaleSlack;
-                if constexpr (FP8) over |= sc[j][x] + ve[x >> 1] > mv[j][x & 1] + kRescaleSlack;
-            }
+            for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    over |= sc[u][j][x] > m[j][x & 1] + kRescaleSlack;
+                    if constexpr (FP8) over |= sc[u][j][x] + ve[u][x >> 1] > mv[j][x & 1] + kRescaleSlack;
+                }
         }
         // lazy rescaling, as in attn_warp.cuh: the references move only when some score is
         // more than 2^8 above them
@@ -550,13 +590,19 @@ row_attention_kernel(const RowParams p) {
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float mn = fmaxf(m[j][x], max_over_keys(fmaxf(sc[j][x], sc[j][2 + x])));
+                    float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u) {
+                        top = fmaxf(top, fmaxf(sc[u][j][x], sc[u][j][2 + x]));
+                        topv = fmaxf(topv, fmaxf(sc[u][j][x] + ve[u][0], sc[u][j][2 + x] + ve[u][1]));
+                    }
+                    const float mn = fmaxf(m[j][x], max_over_keys(top));
                     const float al = mn > m[j][x] ? fast_exp2(m[j][x] - mn) : 1.f;
                     l[j][x] *= al;
                     m[j][x] = mn;
                     float ao = al;
                     if constexpr (FP8) {
-                        const float vn = fmaxf(mv[j][x], max_over_keys(fmaxf(sc[j][x] + ve[0], sc[j][2 + x] + ve[1])));
+                        const float vn = fmaxf(mv[j][x], max_over_keys(topv));
                         ao = vn > mv[j][x] ? fast_exp2(mv[j][x] - vn) : 1.f;
                         mv[j][x] = vn;
                     }
@@ -567,57 +613,68 @@ row_attention_kernel(const RowParams p) {
                     }
                 }
         }
-        uint32_t ph[NT][2], pl[NT][2];
+        uint32_t ph[TILES][NT][2], pl[TILES][NT][2];
         (void)pl;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            float w[4];
+            // a masked score (-inf) weighs 0 also when the row has seen no key yet
+            float base[2], basev[2];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                // a masked score (-inf) weighs 0 also when the row has seen no key yet
-                const bool hide = sc[j][x] == -INFINITY;
-                const float e = hide ? 0.f : fast_exp2(sc[j][x] - m[j][x & 1]);
-                l[j][x & 1] += e;
-                w[x] = e;
-                if constexpr (FP8) w[x] = hide ? 0.f : fast_exp2(sc[j][x] + ve[x >> 1] - mv[j][x & 1]);
+            for (int x = 0; x < 2; ++x) {
+                base[x] = m[j][x] == -INFINITY ? 0.f : m[j][x];
+                basev[x] = mv[j][x] == -INFINITY ? 0.f : mv[j][x];
             }
-            if constexpr (FP8) {
-                ph[j][0] = transpose8x8(pack_half2(w[0], w[1]));
-                ph[j][1] = transpose8x8(pack_half2(w[2], w[3]));
-            } else {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t h = pack_bf16x2(w[2 * y], w[2 * y + 1]);
-                    ph[j][y] = transpose8x8(h);
-                    pl[j][y] = transpose8x8(pack_bf16x2(w[2 * y] - bf16_lo(h), w[2 * y + 1] - bf16_hi(h)));
+            for (int u = 0; u < TILES; ++u) {
+                float w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float e = fast_exp2(sc[u][j][x] - base[x & 1]);
+                    l[j][x & 1] += e;
+                    w[x] = e;
+                    if constexpr (FP8) w[x] = fast_exp2(sc[u][j][x] + (ve[u][x >> 1] - basev[x & 1]));
+                }
+                if constexpr (FP8) {
+                    ph[u][j][0] = transpose8x8(pack_half2(w[0], w[1]));
+                    ph[u][j][1] = transpose8x8(pack_half2(w[2], w[3]));
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t h = pack_bf16x2(w[2 * y], w[2 * y + 1]);
+                        ph[u][j][y] = transpose8x8(h);
+                        pl[u][j][y] = transpose8x8(pack_bf16x2(w[2 * y] - bf16_lo(h), w[2 * y + 1] - bf16_hi(h)));
+                    }
                 }
             }
         }
         // ---- O^T += V^T P^T ----
-        const uint8_t* vs = sb + Stage::KV;
         if constexpr (FP8) {
             constexpr int N = D / 8;   // dims of this lane: g * N ..
-            uint32_t v[4][N / 4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int r = 2 * t + (y & 1) + 8 * (y >> 1);
-                if constexpr (N == 16) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(vs + Stage::at(r, g));
-                    v[y][0] = u.x; v[y][1] = u.y; v[y][2] = u.z; v[y][3] = u.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(vs + Stage::at(r, g >> 1) + (g & 1) * 8);
-                    v[y][0] = u.x; v[y][1] = u.y;
+            for (int u = 0; u < TILES; ++u) {
+                const uint8_t* vs = sb + u * 2 * Stage::KV + Stage::KV;
+                uint32_t v[4][N / 4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int r = 2 * t + (y & 1) + 8 * (y >> 1);
+                    if constexpr (N == 16) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(vs + Stage::at(r, g));
+                        v[y][0] = w.x; v[y][1] = w.y; v[y][2] = w.z; v[y][3] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(vs + Stage::at(r, g >> 1) + (g & 1) * 8);
+                        v[y][0] = w.x; v[y][1] = w.y;
+                    }
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                // dims 2 i, 2 i + 1 of the four keys: (key 2t, key 2t + 1) pairs, then 2t + 8, 2t + 9
-                const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-                uint32_t f[4];
-                e4m3x4_to_half2(__byte_perm(v[0][i / 2], v[1][i / 2], sel), f[0], f[1]);
-                e4m3x4_to_half2(__byte_perm(v[2][i / 2], v[3][i / 2], sel), f[2], f[3]);
+                for (int i = 0; i < MT; ++i) {
+                    // dims 2 i, 2 i + 1 of the four keys: (key 2t, key 2t + 1) pairs, then 2t + 8, 2t + 9
+                    const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+                    uint32_t f[4];
+                    e4m3x4_to_half2(__byte_perm(v[0][i / 2], v[1][i / 2], sel), f[0], f[1]);
+                    e4m3x4_to_half2(__byte_perm(v[2][i / 2], v[3][i / 2], sel), f[2], f[3]);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma_f16(o[j][i], f, ph[j][0], ph[j][1]);
+                    for (int j = 0; j < NT; ++j) mma_f16(o[j][i], f, ph[u][j][0], ph[u][j][1]);
+                }
             }
         } else {
             const int r = (lane & 7) + ((lane >> 4) << 3);
@@ -627,8 +684,8 @@ row_attention_kernel(const RowParams p) {
                 ldmatrix4_trans(f, sa + Stage::KV + Stage::at(r, 2 * i + ((lane >> 3) & 1)));
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    mma_bf16(o[j][i], f, ph[j][0], ph[j][1]);
-                    mma_bf16(o[j][i], f, pl[j][0], pl[j][1]);
+                    mma_bf16(o[j][i], f, ph[0][j][0], ph[0][j][1]);
+                    mma_bf16(o[j][i], f, pl[0][j][0], pl[0][j][1]);
                 }
             }
         }
@@ -679,7 +736,7 @@ row_attention_kernel(const RowParams p) {
 // ------------------------------------------------------------------------------------
 template <int D, bool FP8>
 constexpr int row_smem() {
-    return kRowWarps * row_stages<FP8>() * (RowStage<D, FP8>::BYTES + 48);
+    return kRowWarps * kRowStages * (RowStage<D, FP8>::BYTES + 48);
 }
 
 template <int D, bool FP8, int NT>
