@@ -36,9 +36,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 
 // 16-byte asynchronous global->shared copy; src_bytes = 0 fills the destination with
 // zeros without reading the source.
-__device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src, int src_bytes) {
+__device__ __forceinline__ void cp_async16_to(uint32_t smem_dst, const void* gmem_src, int src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n"
-                 :: "r"(smem_u32(smem_dst)), "l"(gmem_src), "r"(src_bytes) : "memory");
+                 :: "r"(smem_dst), "l"(gmem_src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src, int src_bytes) {
+    cp_async16_to(smem_u32(smem_dst), gmem_src, src_bytes);
 }
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;\n" ::: "memory");

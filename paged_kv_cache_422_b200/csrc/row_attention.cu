@@ -270,7 +270,7 @@ row_attention_kernel(const RowParams p) {
     bool it_valid = false;
     int4 it_a = make_int4(0, 0, 0, 0), it_b = it_a;
     int it_hk = 0, it_v = 0, it_end = 0, it_plast = 0;
-    int it_blk[TILES];
+    int it_blk[TILES] = {};
     TileRange it_r{};
     const int32_t* it_bt = nullptr;
 
@@ -283,7 +283,7 @@ row_attention_kernel(const RowParams p) {
     auto load_block = [&]() {   // the table entries of the stage to be issued next (checked there)
 #pragma unroll
         for (int u = 0; u < TILES; ++u)
-            if (it_v + u < it_end) it_blk[u] = __ldg(it_bt + (real_tile(it_v + u) >> tile_shift));
+            it_blk[u] = it_v + u < it_end ? __ldg(it_bt + (real_tile(it_v + u) >> tile_shift)) : 0;
     };
     auto fetch = [&]() {
         const int idx = __shfl_sync(0xffffffffu, nx_item, 0);
@@ -305,10 +305,19 @@ row_attention_kernel(const RowParams p) {
         load_block();
     };
     // this lane's chunk of rows lane / CHUNKS + i * (32 / CHUNKS)
+    constexpr int COPIES = Stage::CHUNKS / 2, STEP = 32 / Stage::CHUNKS;
     const size_t lane_off = (size_t)(lane / Stage::CHUNKS) * row_bytes + (lane % Stage::CHUNKS) * 16;
-    const size_t row_step = (size_t)(32 / Stage::CHUNKS) * row_bytes;
-    // meta: (real tile, first | last << 1, seen keys, real second tile); tile -1 ends the loop,
-    // -2 is an item without keys
+    const size_t row_step = (size_t)STEP * row_bytes;
+    const uint32_t lane_row = wbase + Stage::at(lane / Stage::CHUNKS, lane % Stage::CHUNKS);
+    const uint32_t lane_row2 = wbase + Stage::at(lane / Stage::CHUNKS + STEP, lane % Stage::CHUNKS);
+    // The swizzle repeats every 8 rows (4 rows of 64 bytes: every 8 too), so copy i goes to
+    // copy i - 2's place plus 2 STEP rows when STEP is 4; otherwise it is computed.
+    auto dst_of = [&](int i) -> uint32_t {
+        if constexpr (STEP == 4) return ((i & 1) ? lane_row2 : lane_row) + (i >> 1) * 8 * Stage::ROW;
+        else return wbase + Stage::at(lane / Stage::CHUNKS + i * STEP, lane % Stage::CHUNKS);
+    };
+    // meta: (real tile, first | last << 1 | open << 2, seen keys, real second tile); tile -1
+    // ends the loop, -2 is an item without keys; an open stage is seen whole by every row
     auto issue = [&](int st) {
         uint8_t* sb = wsm + st * Stage::BYTES;
         int4* meta = reinterpret_cast<int4*>(sb + Stage::META);
@@ -320,47 +329,67 @@ row_attention_kernel(const RowParams p) {
         const bool first = it_v == it_b.y, last = it_v + TILES >= it_end;
         if (it_v < it_end) {
             int tile[2] = {0, 0};
-            uint32_t all_seen = 0;
+            bool open = it_v + TILES <= it_end;
 #pragma unroll
             for (int u = 0; u < TILES; ++u) {
-                const bool have = it_v + u < it_end;
-                tile[u] = real_tile(it_v + (have ? u : 0));
+                tile[u] = real_tile(it_v + (u > 0 && it_v + u < it_end ? u : 0));
                 const int key0 = tile[u] * kTileKeys;
-                // keys that the item's first or any later query token sees
-                uint32_t seen = have ? first_keys(it_plast + 1 - key0) : 0;
-                if (p.window > 0) seen &= ~first_keys(it_b.x - p.window + 1 - key0) | first_keys(p.sinks - key0);
-                int blk = have ? it_blk[u] : it_blk[0];
-                if (blk < 0 || blk >= p.num_blocks) {
-                    if (lane == 0) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
-                    blk = 0;
-                    seen = 0;   // its rows are absent
+                open = open && key0 + kTileKeys - 1 <= it_b.x && it_blk[u] >= 0 && it_blk[u] < p.num_blocks &&
+                       (p.window == 0 || key0 > it_plast - p.window || key0 + kTileKeys <= p.sinks);
+            }
+            uint32_t seen = ALL;
+            if (!open) {
+                seen = 0;
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) {
+                    const bool have = it_v + u < it_end;
+                    const int key0 = tile[u] * kTileKeys;
+                    // keys that the item's first or any later query token sees
+                    uint32_t m = have ? first_keys(it_plast + 1 - key0) : 0;
+                    if (p.window > 0) m &= ~first_keys(it_b.x - p.window + 1 - key0) | first_keys(p.sinks - key0);
+                    if (have && (it_blk[u] < 0 || it_blk[u] >= p.num_blocks)) {
+                        if (lane == 0) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
+                        m = 0;   // its rows are absent
+                    }
+                    if (m == 0) it_blk[u] = 0;   // nothing is read
+                    seen |= m << (16 * u);
                 }
-                const int row0 = key0 & (p.block_size - 1);
-                const size_t off = ((size_t)blk * p.block_size + row0) * row_bytes + (size_t)it_hk * Stage::ROW + lane_off;
+            }
+            const uint32_t sd = (uint32_t)(st * Stage::BYTES);
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+                const size_t off = ((size_t)it_blk[u] * p.block_size + (tile[u] * kTileKeys & (p.block_size - 1))) * row_bytes +
+                                   (size_t)it_hk * Stage::ROW + lane_off;
                 const uint8_t* kg = static_cast<const uint8_t*>(p.k_cache) + off;
                 const uint8_t* vg = static_cast<const uint8_t*>(p.v_cache) + off;
-                uint8_t* kd = sb + u * 2 * Stage::KV;
-                auto copy = [&](bool whole) {
+                const uint32_t kd = sd + u * 2 * Stage::KV;
+                if (open) {
 #pragma unroll
-                    for (int i = 0; i < Stage::CHUNKS / 2; ++i) {
-                        const int r = lane / Stage::CHUNKS + i * (32 / Stage::CHUNKS);
-                        const int nb = whole || ((seen >> r) & 1) ? 16 : 0;   // 0: zero-filled, not read
-                        const int at = Stage::at(r, lane % Stage::CHUNKS);
-                        cp_async16(kd + at, kg + i * row_step, nb);
-                        cp_async16(kd + Stage::KV + at, vg + i * row_step, nb);
+                    for (int i = 0; i < COPIES; ++i, kg += row_step, vg += row_step) {
+                        cp_async16_to(dst_of(i) + kd, kg, 16);
+                        cp_async16_to(dst_of(i) + kd + Stage::KV, vg, 16);
                     }
-                };
-                if (seen == 0xffffu) copy(true);
-                else copy(false);
-                if constexpr (FP8) {
-                    if (lane < 2) {
-                        const size_t so = ((size_t)blk * p.hkv + it_hk) * p.block_size + row0;
-                        cp_async16(sb + Stage::SCALES + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + so, 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < COPIES; ++i, kg += row_step, vg += row_step) {
+                        // 0: zero-filled, not read
+                        const int nb = (seen >> (16 * u + lane / Stage::CHUNKS + i * STEP)) & 1 ? 16 : 0;
+                        cp_async16_to(dst_of(i) + kd, kg, nb);
+                        cp_async16_to(dst_of(i) + kd + Stage::KV, vg, nb);
                     }
                 }
-                all_seen |= seen << (16 * u);
             }
-            if (lane == 0) *meta = make_int4(tile[0], (first ? 1 : 0) | (last ? 2 : 0), (int)all_seen, tile[1]);
+            if constexpr (FP8) {
+                // lane 2 u + v: the K (v = 0) or V scales of tile u
+                if (lane < 2 * TILES) {
+                    const int u = lane >> 1;
+                    const size_t so = ((size_t)(u ? it_blk[TILES - 1] : it_blk[0]) * p.hkv + it_hk) * p.block_size +
+                                      ((u ? tile[1] : tile[0]) * kTileKeys & (p.block_size - 1));
+                    cp_async16_to(wbase + sd + Stage::SCALES + lane * 16, ((lane & 1) ? p.v_scales : p.k_scales) + so, 16);
+                }
+            }
+            if (lane == 0)
+                *meta = make_int4(tile[0], (first ? 1 : 0) | (last ? 2 : 0) | (open ? 4 : 0), (int)seen, tile[1]);
         } else if (lane == 0) {
             *meta = make_int4(-2, 3, 0, 0);
         }
@@ -377,12 +406,13 @@ row_attention_kernel(const RowParams p) {
     int pos[NT][2];                // their positions (-1: no such row)
     float o[NT][MT][4];
     float m[NT][2], mv[NT][2], l[NT][2];
-    (void)mv;
+    uint32_t unset = 0;            // rows (bit 2 j + x) that have seen no key: their m and mv mean nothing yet
 
     auto start = [&](const int4& na, const int4& nb, int nhk) {
         a = na;
         b = nb;
         hk = nhk;
+        unset = 0;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             // Q^T fragment: row n = 8 j + g, the dims that this lane's K chunks hold
@@ -427,8 +457,8 @@ row_attention_kernel(const RowParams p) {
                 qs[j][x] = __shfl_sync(0xffffffffu, fac, (2 * t + x) * 4);
                 const int r = 8 * j + 2 * t + x, rt = r / p.group;
                 pos[j][x] = rt < a.w ? b.x + rt : -1;
-                m[j][x] = mv[j][x] = -INFINITY;
-                l[j][x] = 0.f;
+                m[j][x] = mv[j][x] = l[j][x] = 0.f;
+                if (pos[j][x] >= 0) unset |= 1u << (2 * j + x);
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
@@ -552,87 +582,100 @@ row_attention_kernel(const RowParams p) {
                     ve[u][y] = (float)((int)ss[16] - 127);
                 }
             }
-        // tiles that every row sees whole need no mask (rows that do not exist may see them)
-        bool open = (uint32_t)meta.z == ALL;
-#pragma unroll
-        for (int u = 0; u < TILES; ++u)
-            open = open && key0[u] + kTileKeys - 1 <= b.x &&
-                   (p.window == 0 || key0[u] > b.x + a.w - 1 - p.window || key0[u] + kTileKeys <= p.sinks);
-        bool over = false;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        // Exponents against the rows' references: sc - m for the sum, and for the e4m3 weights
+        // (which carry the value's 2^ve) sc + ve - mv.  `arg` turns raw scores into them.
+        float ew[TILES][NT][4];
+        (void)ew;
+        auto arg = [&](int j) {
 #pragma unroll
             for (int u = 0; u < TILES; ++u)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sc[u][j][x] *= FP8 ? qs[j][x & 1] * kf[u][x >> 1] : qs[j][x & 1];
-            if (!open) {
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (FP8) {
+                        const float f = qs[j][x & 1] * kf[u][x >> 1];
+                        ew[u][j][x] = fmaf(sc[u][j][x], f, ve[u][x >> 1] - mv[j][x & 1]);
+                        sc[u][j][x] = fmaf(sc[u][j][x], f, -m[j][x & 1]);
+                    } else {
+                        sc[u][j][x] = fmaf(sc[u][j][x], qs[j][x & 1], -m[j][x & 1]);
+                    }
+                }
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            arg(j);
+            // keys that a row does not see weigh 0 (rows that do not exist may see them)
+            if (!(meta.y & 4)) {
 #pragma unroll
                 for (int u = 0; u < TILES; ++u)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t seen = seen_keys(key0[u], pos[j][x], p.window, p.sinks) & ((uint32_t)meta.z >> (16 * u));
-                        if (!((seen >> g) & 1)) sc[u][j][x] = -INFINITY;
-                        if (!((seen >> (g + 8)) & 1)) sc[u][j][2 + x] = -INFINITY;
+                        if (!((seen >> g) & 1)) sc[u][j][x] = ew[u][j][x] = -INFINITY;
+                        if (!((seen >> (g + 8)) & 1)) sc[u][j][2 + x] = ew[u][j][2 + x] = -INFINITY;
                     }
             }
 #pragma unroll
             for (int u = 0; u < TILES; ++u)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    over |= sc[u][j][x] > m[j][x & 1] + kRescaleSlack;
-                    if constexpr (FP8) over |= sc[u][j][x] + ve[u][x >> 1] > mv[j][x & 1] + kRescaleSlack;
+                    top = fmaxf(top, sc[u][j][x]);
+                    if constexpr (FP8) top = fmaxf(top, ew[u][j][x]);
                 }
         }
-        // lazy rescaling, as in attn_warp.cuh: the references move only when some score is
-        // more than 2^8 above them
-        if (__any_sync(0xffffffffu, over)) {
+        // lazy rescaling, as in attn_warp.cuh: the references move only when some exponent is
+        // more than kRescaleSlack above them, and when a row sees its first keys
+        if (__any_sync(0xffffffffu, top > kRescaleSlack || unset != 0)) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float top = -INFINITY, topv = -INFINITY;
+                    float up = -INFINITY, upv = -INFINITY;   // how far the references move
 #pragma unroll
                     for (int u = 0; u < TILES; ++u) {
-                        top = fmaxf(top, fmaxf(sc[u][j][x], sc[u][j][2 + x]));
-                        topv = fmaxf(topv, fmaxf(sc[u][j][x] + ve[u][0], sc[u][j][2 + x] + ve[u][1]));
+                        up = fmaxf(up, fmaxf(sc[u][j][x], sc[u][j][2 + x]));
+                        if constexpr (FP8) upv = fmaxf(upv, fmaxf(ew[u][j][x], ew[u][j][2 + x]));
                     }
-                    const float mn = fmaxf(m[j][x], max_over_keys(top));
-                    const float al = mn > m[j][x] ? fast_exp2(m[j][x] - mn) : 1.f;
+                    up = max_over_keys(up);
+                    upv = FP8 ? max_over_keys(upv) : up;
+                    const uint32_t bit = 1u << (2 * j + x);
+                    const bool fresh = (unset & bit) != 0, some = up > -INFINITY;
+                    if (!fresh) {
+                        up = fmaxf(up, 0.f);
+                        upv = fmaxf(upv, 0.f);
+                    }
+                    if (!some) up = upv = 0.f;
+                    else unset &= ~bit;
+                    m[j][x] += up;
+                    mv[j][x] += upv;
+                    const float al = fresh ? 1.f : fast_exp2(-up), ao = fresh ? 1.f : fast_exp2(-upv);
                     l[j][x] *= al;
-                    m[j][x] = mn;
-                    float ao = al;
-                    if constexpr (FP8) {
-                        const float vn = fmaxf(mv[j][x], max_over_keys(topv));
-                        ao = vn > mv[j][x] ? fast_exp2(mv[j][x] - vn) : 1.f;
-                        mv[j][x] = vn;
-                    }
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         o[j][i][x] *= ao;
                         o[j][i][2 + x] *= ao;
                     }
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                        for (int y = 0; y < 4; y += 2) {
+                            sc[u][j][x + y] -= up;
+                            if constexpr (FP8) ew[u][j][x + y] -= upv;
+                        }
                 }
         }
         uint32_t ph[TILES][NT][2], pl[TILES][NT][2];
         (void)pl;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            // a masked score (-inf) weighs 0 also when the row has seen no key yet
-            float base[2], basev[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                base[x] = m[j][x] == -INFINITY ? 0.f : m[j][x];
-                basev[x] = mv[j][x] == -INFINITY ? 0.f : mv[j][x];
-            }
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int u = 0; u < TILES; ++u) {
                 float w[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float e = fast_exp2(sc[u][j][x] - base[x & 1]);
+                    const float e = fast_exp2(sc[u][j][x]);
                     l[j][x & 1] += e;
-                    w[x] = e;
-                    if constexpr (FP8) w[x] = fast_exp2(sc[u][j][x] + (ve[u][x >> 1] - basev[x & 1]));
+                    w[x] = FP8 ? fast_exp2(ew[u][j][x]) : e;
                 }
                 if constexpr (FP8) {
                     ph[u][j][0] = transpose8x8(pack_half2(w[0], w[1]));
@@ -646,7 +689,6 @@ row_attention_kernel(const RowParams p) {
                     }
                 }
             }
-        }
         // ---- O^T += V^T P^T ----
         if constexpr (FP8) {
             constexpr int N = D / 8;   // dims of this lane: g * N ..
