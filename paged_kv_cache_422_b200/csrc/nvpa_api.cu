@@ -454,7 +454,7 @@ size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int n
         !window_sizes_ok(num_q_heads, num_kv_heads, head_dim, max_context_len, window, num_sinks, num_splits))
         return 0;
     return row_attention_workspace_bytes(batch, batch, 1, num_q_heads, num_kv_heads, head_dim, max_context_len,
-                                         block_size, window, num_sinks, num_splits);
+                                         window, num_sinks, num_splits);
 }
 
 nvpa_status_t nvpa_paged_decode_attention_window(
@@ -491,7 +491,7 @@ size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_hea
                ? chunk_tiles_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
                                              max_context_len, window, num_sinks, num_splits)
                : row_attention_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
-                                               max_context_len, block_size, window, num_sinks, num_splits);
+                                               max_context_len, window, num_sinks, num_splits);
 }
 
 nvpa_status_t nvpa_chunk_attention(

@@ -146,7 +146,7 @@ nvpa_status_t run_gather_kv_fp8(void* dst, const void* cache, const uint8_t* sca
                                 int num_blocks, int block_size, int32_t* err_flag, cudaStream_t stream);
 // Few query rows per KV head (row_attention.cu).
 size_t row_attention_workspace_bytes(int batch, int total_q, int max_q, int hq, int hkv, int head_dim,
-                                     int max_ctx, int block_size, int window, int sinks, int num_splits);
+                                     int max_ctx, int window, int sinks, int num_splits);
 nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream);
 // Long chunks, on the tensor cores (chunk_tcgen05.cu).
 size_t chunk_tiles_workspace_bytes(int batch, int total_q, int max_q, int hq, int hkv, int head_dim, int max_ctx,

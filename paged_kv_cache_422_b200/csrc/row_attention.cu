@@ -820,8 +820,29 @@ struct RowGeometry {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// 16-key tiles per partition, from host-side bounds only (a captured call keeps its launches and
+// its workspace, and a sequence's partitions do not depend on the others' lengths).  `pairs`
+// row tiles times KV heads see `seen` tiles each at most.
+//  - Many pairs (more than an eighth of the resident warps): 22 tiles, many rounds of items
+//    whose varying lengths even the rounds out (64 contexts of 0.5 to 4 k keys in 8 bits: 73 us;
+//    28 tiles 77, 18 tiles 80, 37 tiles 84).
+//  - Few long ones: as many partitions as keep every item in one round, less a tenth for
+//    lengths that the host does not know (8 contexts of 32 k keys: 24 partitions each 107 us,
+//    27 109, 30, where a second round begins, 146, 64 124).
+// Four tiles at least: shorter items cost more than the warps they fill.
+int row_chunk_tiles(long long pairs, long long seen, int nt, int num_splits) {
+    if (num_splits > 0) return (int)std::max(1LL, (seen + num_splits - 1) / num_splits);
+    const long long warps = 148LL * kRowWarps * (nt == 1 ? 3 : 2);   // resident on a B200
+    long long chunk = 22;
+    if (pairs * 8 <= warps) {
+        const long long parts = std::max(1LL, warps * 9 / 10 / std::max(1LL, pairs));
+        chunk = std::max(4LL, (seen + parts - 1) / parts);
+    }
+    return (int)std::min(chunk, seen);
+}
+
 RowGeometry row_geometry(int batch, int total_q, int max_q, int hq, int hkv, int head_dim, int max_ctx,
-                         int block_size, int window, int sinks, int num_splits) {
+                         int window, int sinks, int num_splits) {
     RowGeometry r{};
     const int group = std::max(1, hq / hkv);
     r.nt = max_q * group <= 8 ? 1 : 2;
@@ -834,9 +855,7 @@ RowGeometry row_geometry(int batch, int total_q, int max_q, int hq, int hkv, int
         seen = std::min(seen, ((long long)window + r.tok + kTileKeys - 2) / kTileKeys + 1 +
                                   ((long long)sinks + kTileKeys - 1) / kTileKeys);
     seen = std::max(1LL, seen);
-    const int eff = (int)std::min<long long>(seen * kTileKeys, 0x7ffffff0);
-    const int per = decode_chunk_keys((int)std::min<long long>(r.tiles, 0x7fffffff), hkv, eff, block_size, num_splits);
-    r.chunk = per / kTileKeys;
+    r.chunk = row_chunk_tiles(r.tiles * hkv, seen, r.nt, num_splits);
     // the partition index travels in 15 bits
     r.chunk = (int)std::max<long long>(r.chunk, (seen + 32766) / 32767);
     r.s_max = (int)((seen + r.chunk - 1) / r.chunk);
@@ -853,13 +872,13 @@ RowGeometry row_geometry(int batch, int total_q, int max_q, int hq, int hkv, int
 }  // namespace
 
 size_t row_attention_workspace_bytes(int batch, int total_q, int max_q, int hq, int hkv, int head_dim,
-                                     int max_ctx, int block_size, int window, int sinks, int num_splits) {
-    return row_geometry(batch, total_q, max_q, hq, hkv, head_dim, max_ctx, block_size, window, sinks, num_splits).total;
+                                     int max_ctx, int window, int sinks, int num_splits) {
+    return row_geometry(batch, total_q, max_q, hq, hkv, head_dim, max_ctx, window, sinks, num_splits).total;
 }
 
 nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     const RowGeometry r = row_geometry(c.batch, c.total_q, c.max_seqlen_q, c.hq, c.hkv, c.head_dim,
-                                       c.max_context_len, c.block_size, c.window, c.num_sinks, c.num_splits);
+                                       c.max_context_len, c.window, c.num_sinks, c.num_splits);
     if (c.workspace_bytes < r.total) {
         set_error("workspace too small: %zu bytes given, %zu needed", c.workspace_bytes, r.total);
         return NVPA_ERR_WORKSPACE_TOO_SMALL;
