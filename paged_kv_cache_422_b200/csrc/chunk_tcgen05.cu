@@ -54,9 +54,7 @@ namespace {
 
 constexpr int kRows = 128;        // query rows per tile (MMA M)
 constexpr int kKeys = 128;        // keys per tile
-constexpr int kRing = 4;          // K/V tiles in bf16, ready for the MMAs
 constexpr int kUnits = 4;         // claimed units handed from the producer to the others
-constexpr int kStageRing = 2;     // staged e4m3 tiles
 constexpr int kBuckets = 4096;    // plan: key-tile counts sorted exactly
 constexpr int kGran = 16;         // granularity of the virtual key range
 
@@ -69,7 +67,12 @@ struct Roles {
     static constexpr int SMALL_REGS = FP8 ? 64 : 104;      // warps 0..3 and 12..15
     static constexpr int SOFTMAX_REGS = FP8 ? 192 : 200;   // warps 4..11
     static constexpr int READERS = 1 + 8 + (FP8 ? 4 : 0);  // of the unit ring
+    // shared memory at head_dim 128: Q tiles and K/V tiles (bf16, ready for the MMAs) of 32 KB,
+    // staged e4m3 tiles of 16 KB.  A tile takes 2 us from its copy's issue to its arrival, so
+    // the e4m3 cache's copies run four tiles ahead of the widening.
     static constexpr int QBUFS = FP8 ? 2 : 3;
+    static constexpr int RING = FP8 ? 3 : 4;
+    static constexpr int STAGES = FP8 ? 4 : 1;
     static_assert((WARPS - 8) * SMALL_REGS + 8 * SOFTMAX_REGS == WARPS * LAUNCH_REGS, "register split");
     static_assert(((WARPS - 8) / 4 * SMALL_REGS + 2 * SOFTMAX_REGS) * 32 <= 16384, "sub-partition registers");
 };
@@ -109,19 +112,19 @@ struct ChunkLayout {
     static constexpr int TILE_BYTES = REGIONS * REGION_BYTES;
     static constexpr int Q_OFF = 0;
     static constexpr int RING_OFF = R::QBUFS * TILE_BYTES;
-    static constexpr int STAGE_OFF = RING_OFF + kRing * TILE_BYTES;      // codes [128 rows][D]
+    static constexpr int STAGE_OFF = RING_OFF + R::RING * TILE_BYTES;      // codes [128 rows][D]
     static constexpr int STAGE_BYTES = FP8 ? kKeys * D : 0;
-    static constexpr int SCALE_OFF = STAGE_OFF + kStageRing * STAGE_BYTES;   // 128 scale bytes each
-    static constexpr int BAR_OFF = SCALE_OFF + (FP8 ? kStageRing * kKeys : 0);
+    static constexpr int SCALE_OFF = STAGE_OFF + R::STAGES * STAGE_BYTES;   // 128 scale bytes each
+    static constexpr int BAR_OFF = SCALE_OFF + (FP8 ? R::STAGES * kKeys : 0);
     // barriers (per query tile in pairs: + 0 for A, + 1 for B)
-    static constexpr int B_QFULL = 0, B_QEMPTY = R::QBUFS, B_KVFULL = 2 * R::QBUFS, B_KVEMPTY = B_KVFULL + kRing;
-    static constexpr int B_SFULL = B_KVEMPTY + kRing, B_PFULL = B_SFULL + 2, B_ODONE = B_PFULL + 2;
+    static constexpr int B_QFULL = 0, B_QEMPTY = R::QBUFS, B_KVFULL = 2 * R::QBUFS, B_KVEMPTY = B_KVFULL + R::RING;
+    static constexpr int B_SFULL = B_KVEMPTY + R::RING, B_PFULL = B_SFULL + 2, B_ODONE = B_PFULL + 2;
     static constexpr int B_OFINAL = B_ODONE + 2, B_OFREE = B_OFINAL + 2, B_DRAIN = B_OFREE + 2;
     static constexpr int B_UFULL = B_DRAIN + 1, B_UEMPTY = B_UFULL + kUnits;
-    static constexpr int B_STFULL = B_UEMPTY + kUnits, B_STEMPTY = B_STFULL + kStageRing;
-    static constexpr int NBARS = B_STEMPTY + kStageRing;
+    static constexpr int B_STFULL = B_UEMPTY + kUnits, B_STEMPTY = B_STFULL + R::STAGES;
+    static constexpr int NBARS = B_STEMPTY + R::STAGES;
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;     // tmem base, abort flag, staged piece masks
-    static constexpr int UNIT_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+    static constexpr int UNIT_OFF = (MISC_OFF + 8 + 4 * R::STAGES + 15) / 16 * 16;
     static constexpr int BYTES = UNIT_OFF + 32 * kUnits;
     static constexpr int ALLOC = BYTES + 1024;               // room to align the base to 1024
 };
@@ -283,18 +286,53 @@ __device__ __forceinline__ void mask_columns(uint32_t (&sv)[kKeys], int base, in
     }
 }
 
-// 16 e4m3 codes times f as bf16 (f a power of two: exact).
-__device__ __forceinline__ void widen16(const uint4& u, float f, uint4& lo, uint4& hi) {
+// 16 e4m3 codes times 2^(byte - 127) as bf16.  The products are exact (4 significant bits), so
+// the upper halves of their float32 forms are their bf16 forms.  A scale that is an fp16 value
+// (2^-24 .. 2^15: rows of magnitude up to 2^-16 .. 2^24) goes through the mixed-precision FMA,
+// which widens and scales in one instruction: 4.3 ns per warp and 32-bit word against 6.2 for
+// conversion, multiplication and packing.
+struct RowScale {
+    uint16_t half;    // 0: outside fp16
+    float value;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t byte) {
+    RowScale r;
+    r.value = scale_value(byte);
+    r.half = byte > 142 || byte < 103 ? 0 : (uint16_t)(byte >= 113 ? (byte - 112) << 10 : 1u << (byte - 103));
+    return r;
+}
+__device__ __forceinline__ uint32_t scale_half2(uint32_t h2, uint16_t f) {
+    float x, y;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "fma.rn.f32.f16 %0, a, %3, %4;\n\tfma.rn.f32.f16 %1, b, %3, %4;\n\t}"
+        : "=f"(x), "=f"(y) : "r"(h2), "h"(f), "f"(0.f));
+    return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
+__device__ __forceinline__ void widen16(const uint4& u, uint16_t f, uint4& lo, uint4& hi) {
     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t a, b;
-        e4m3x4_to_half2(in[i], a, b);
-        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&a));
-        const float2 y = __half22float2(*reinterpret_cast<__half2*>(&b));
-        w[2 * i] = pack_bf16x2(x.x * f, x.y * f);
-        w[2 * i + 1] = pack_bf16x2(y.x * f, y.y * f);
+        e4m3x4_to_half2(in[i], w[2 * i], w[2 * i + 1]);
+        w[2 * i] = scale_half2(w[2 * i], f);
+        w[2 * i + 1] = scale_half2(w[2 * i + 1], f);
+    }
+    lo = make_uint4(w[0], w[1], w[2], w[3]);
+    hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+// The same for any scale.
+__device__ __forceinline__ void widen16_any(const uint4& u, float f, uint4& lo, uint4& hi) {
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2];
+        e4m3x4_to_half2(in[i], h[0], h[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h[k]));
+            w[2 * i + k] = pack_bf16x2(x.x * f, x.y * f);
+        }
     }
     lo = make_uint4(w[0], w[1], w[2], w[3]);
     hi = make_uint4(w[4], w[5], w[6], w[7]);
@@ -332,11 +370,11 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             mbar_init(bars + L::B_QFULL + q, 1);
             mbar_init(bars + L::B_QEMPTY + q, 1);
         }
-        for (int s = 0; s < kRing; ++s) {
+        for (int s = 0; s < R::RING; ++s) {
             mbar_init(bars + L::B_KVFULL + s, FP8 ? 4 : 1);
             mbar_init(bars + L::B_KVEMPTY + s, 1);
         }
-        for (int s = 0; s < kStageRing; ++s) {
+        for (int s = 0; s < R::STAGES; ++s) {
             mbar_init(bars + L::B_STFULL + s, 1);
             mbar_init(bars + L::B_STEMPTY + s, 4);
         }
@@ -448,7 +486,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             // K (kv = 0) or V of key tile j, whose block ids the lanes hold.  A block id out of
             // range is flagged (once, with K) and its rows are zero: their keys score 0 and add 0.
             auto load_kv = [&](int kv, int j, int blk_lane) -> bool {
-                constexpr int RING = FP8 ? kStageRing : kRing;
+                constexpr int RING = FP8 ? R::STAGES : R::RING;
                 const int slot = fill % RING;
                 uint64_t* full = bars + (FP8 ? L::B_STFULL : L::B_KVFULL) + slot;
                 if (!mbar_wait(bars + (FP8 ? L::B_STEMPTY : L::B_KVEMPTY) + slot, ((fill / RING) & 1) ^ 1,
@@ -523,7 +561,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     }
                 }
             };
-            drain(bars + (FP8 ? L::B_STFULL : L::B_KVFULL), fill, FP8 ? kStageRing : kRing);
+            drain(bars + (FP8 ? L::B_STFULL : L::B_KVFULL), fill, FP8 ? R::STAGES : R::RING);
             drain(bars + L::B_QFULL, qfill, QBUFS);
         }
       } else if (warp == 1) {
@@ -567,7 +605,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const int nkv = max(nk[0], nk[1]);
             const int v0 = u.part * p.chunk * kKeys;
             // S of key tile 0: tile A as soon as Q_A and K_0 are in, then tile B
-            if (!mbar_wait(bars + L::B_KVFULL + fbase % kRing, (fbase / kRing) & 1, abort_flag, p.err)) break;
+            if (!mbar_wait(bars + L::B_KVFULL + fbase % R::RING, (fbase / R::RING) & 1, abort_flag, p.err)) break;
             uint32_t qsl[2] = {0, 0};
             for (int x = 0; x < 2 && ok; ++x) {
                 if (nk[x] == 0) continue;
@@ -579,18 +617,18 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 ++qcons;
                 tc_fence_after();
                 if (lane == 0) {
-                    issue_qk(x, fbase % kRing, qsl[x]);
+                    issue_qk(x, fbase % R::RING, qsl[x]);
                     if (nk[x] == 1) umma_commit(bars + L::B_QEMPTY + qsl[x]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) umma_commit(bars + L::B_KVEMPTY + fbase % kRing);
+            if (lane == 0) umma_commit(bars + L::B_KVEMPTY + fbase % R::RING);
             __syncwarp();
             for (int j = 0; j < nkv && ok; ++j) {
                 const uint32_t fv = fbase + 2 * (uint32_t)j + 1, fk = fv + 1;
-                const int vslot = fv % kRing, kslot = fk % kRing;
-                if (!mbar_wait(bars + L::B_KVFULL + vslot, (fv / kRing) & 1, abort_flag, p.err)) {
+                const int vslot = fv % R::RING, kslot = fk % R::RING;
+                if (!mbar_wait(bars + L::B_KVFULL + vslot, (fv / R::RING) & 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
@@ -637,7 +675,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     __syncwarp();
                     if (j + 1 < nk[x]) {
                         if (!k_next) {
-                            if (!mbar_wait(bars + L::B_KVFULL + kslot, (fk / kRing) & 1, abort_flag, p.err)) {
+                            if (!mbar_wait(bars + L::B_KVFULL + kslot, (fk / R::RING) & 1, abort_flag, p.err)) {
                                 ok = false;
                                 break;
                             }
@@ -831,8 +869,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 const int nkv = max(pair_tile(p, u, keys, 0).nkv, pair_tile(p, u, keys, 1).nkv);
                 const int v0 = u.part * p.chunk * kKeys;
                 for (int j = 0; j < 2 * nkv && ok; ++j, ++fill) {   // K_0, V_0, K_1, ...
-                    const int slot = fill % kStageRing, ring = fill % kRing;
-                    if (!mbar_wait(bars + L::B_STFULL + slot, (fill / kStageRing) & 1, abort_flag, p.err)) {
+                    const int slot = fill % R::STAGES, ring = fill % R::RING;
+                    if (!mbar_wait(bars + L::B_STFULL + slot, (fill / R::STAGES) & 1, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
@@ -840,7 +878,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     const int key = keys.real(v0 + (j >> 1) * kKeys + r);
                     const bool seen = ((stage_mask[slot] >> prow) & 1) && key <= keys.p_last &&
                                       (p.window == 0 || key > keys.p_first - p.window || key < p.sinks);
-                    const float f = scale_value(smem[L::SCALE_OFF + slot * kKeys + r]);
+                    const RowScale f = row_scale(smem[L::SCALE_OFF + slot * kKeys + r]);
                     const uint8_t* src = smem + L::STAGE_OFF + slot * L::STAGE_BYTES + r * D;
                     // 128-byte rows: chunk c lies at c ^ (r % 8); 64-byte rows: at c ^ (r / 2 % 4)
                     const int sx = D == 128 ? r & 7 : (r >> 1) & 3;
@@ -848,26 +886,37 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)
                         code[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sx) << 4));
-                    if (!mbar_wait(bars + L::B_KVEMPTY + ring, ((fill / kRing) & 1) ^ 1, abort_flag, p.err)) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + L::B_STEMPTY + slot);   // the codes are in registers
+                    if (!mbar_wait(bars + L::B_KVEMPTY + ring, ((fill / R::RING) & 1) ^ 1, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
                     uint8_t* dst = smem + L::RING_OFF + ring * L::TILE_BYTES + r * 128;
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint4 lo, hi;
-                        widen16(code[c], f, lo, hi);
-                        if (!seen) lo = hi = make_uint4(0, 0, 0, 0);
+                    auto put = [&](int c, const uint4& lo, const uint4& hi) {
                         uint8_t* d = dst + (c / 4) * L::REGION_BYTES;
                         *reinterpret_cast<uint4*>(d + ((((c % 4) * 2) ^ (r & 7)) << 4)) = lo;
                         *reinterpret_cast<uint4*>(d + ((((c % 4) * 2 + 1) ^ (r & 7)) << 4)) = hi;
+                    };
+                    if (__all_sync(0xffffffffu, seen && f.half != 0)) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint4 lo, hi;
+                            widen16(code[c], f.half, lo, hi);
+                            put(c, lo, hi);
+                        }
+                    } else {   // a warp with a special row
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint4 lo, hi;
+                            widen16_any(code[c], f.value, lo, hi);
+                            if (!seen) lo = hi = make_uint4(0, 0, 0, 0);
+                            put(c, lo, hi);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bars + L::B_STEMPTY + slot);
-                        mbar_arrive(bars + L::B_KVFULL + ring);
-                    }
+                    if (lane == 0) mbar_arrive(bars + L::B_KVFULL + ring);
                 }
             }
         }
