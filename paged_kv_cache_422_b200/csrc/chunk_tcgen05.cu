@@ -30,7 +30,7 @@
 // arithmetic that would keep a NaN), and blocks without a visible key are not looked up.
 //
 // Warp roles (one persistent CTA per SM, units claimed longest first):
-//   warp 0       copies Q and K/V tiles by TMA (e4m3: codes and scales into a staging ring);
+//   warps 0 2 3  copy Q and K/V tiles by TMA (e4m3: codes and scales into a staging ring);
 //   warp 1       issues the MMAs: S_A0 S_B0 | O_A += P_A0 V_0, S_A1, O_B += P_B0 V_0, ...;
 //   warps 4..11  softmax of tiles A and B, one thread per row;
 //   warps 12..15 (e4m3 only) widen staged codes into the K/V ring, one thread per key row.
@@ -54,6 +54,7 @@ namespace {
 
 constexpr int kRows = 128;        // query rows per tile (MMA M)
 constexpr int kKeys = 128;        // keys per tile
+constexpr int kProducers = 3;     // warps that issue copies: 0, 2 and 3
 constexpr int kUnits = 4;         // claimed units handed from the producer to the others
 constexpr int kBuckets = 4096;    // plan: key-tile counts sorted exactly
 constexpr int kGran = 16;         // granularity of the virtual key range
@@ -66,7 +67,7 @@ struct Roles {
     static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
     static constexpr int SMALL_REGS = FP8 ? 64 : 104;      // warps 0..3 and 12..15
     static constexpr int SOFTMAX_REGS = FP8 ? 192 : 200;   // warps 4..11
-    static constexpr int READERS = 1 + 8 + (FP8 ? 4 : 0);  // of the unit ring
+    static constexpr int READERS = 1 + 2 + 8 + (FP8 ? 4 : 0);  // of the unit ring
     // shared memory at head_dim 128: Q tiles and K/V tiles (bf16, ready for the MMAs) of 32 KB,
     // staged e4m3 tiles of 16 KB.  A tile takes 2 us from its copy's issue to its arrival, so
     // the e4m3 cache's copies run four tiles ahead of the widening.
@@ -124,7 +125,7 @@ struct ChunkLayout {
     static constexpr int B_STFULL = B_UEMPTY + kUnits, B_STEMPTY = B_STFULL + R::STAGES;
     static constexpr int NBARS = B_STEMPTY + R::STAGES;
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;     // tmem base, abort flag, staged piece masks
-    static constexpr int UNIT_OFF = (MISC_OFF + 8 + 4 * R::STAGES + 15) / 16 * 16;
+    static constexpr int UNIT_OFF = (MISC_OFF + 8 + 4 * kProducers * R::STAGES + 15) / 16 * 16;
     static constexpr int BYTES = UNIT_OFF + 32 * kUnits;
     static constexpr int ALLOC = BYTES + 1024;               // room to align the base to 1024
 };
@@ -353,7 +354,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
-    uint32_t* stage_mask = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF + 8);   // pieces present
+    uint32_t* stage_mask = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF + 8);   // [stage][producer] its pieces present
     ChunkUnit* unit_ring = reinterpret_cast<ChunkUnit*>(smem + L::UNIT_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -371,11 +372,11 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             mbar_init(bars + L::B_QEMPTY + q, 1);
         }
         for (int s = 0; s < R::RING; ++s) {
-            mbar_init(bars + L::B_KVFULL + s, FP8 ? 4 : 1);
+            mbar_init(bars + L::B_KVFULL + s, FP8 ? 4 : kProducers);
             mbar_init(bars + L::B_KVEMPTY + s, 1);
         }
         for (int s = 0; s < R::STAGES; ++s) {
-            mbar_init(bars + L::B_STFULL + s, 1);
+            mbar_init(bars + L::B_STFULL + s, kProducers);
             mbar_init(bars + L::B_STEMPTY + s, 4);
         }
         mbar_init(bars + L::B_DRAIN, 1);
@@ -418,12 +419,18 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
 
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::SMALL_REGS));
-      if (warp == 0) {
-        // ============================ producer ============================
+      if (warp != 1) {
+        // ============================ producers ============================
+        // Three warps copy every tile together, a third of its pieces each: with 16-row pieces
+        // one issuing thread needs 200 cycles per piece and 64 columns, 6600 for the 32 of a K
+        // and V tile, where the MMAs and softmaxes of a pair need half of that.
+        const int pw = warp == 0 ? 0 : warp - 1;
+        const int pc = pw + kProducers * lane;     // this lane's piece of every tile
         uint32_t fill = 0, qfill = 0;
         constexpr int kNoPiece = INT_MIN;
         const int piece = p.piece;
-        // Units are claimed one ahead of the one whose copies are issued.
+        const bool has_piece = pc * piece < kKeys;
+        // Warp 0 claims units, one ahead of the one whose copies are issued.
         auto claim_next = [&]() -> int { return lane == 0 ? atomicAdd(p.counter, 1) : 0; };
         auto describe = [&](int pending) -> ChunkUnit {
             const int i = __shfl_sync(0xffffffffu, pending, 0);
@@ -441,35 +448,46 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             }
             return u;
         };
-        ChunkUnit cur = describe(claim_next());
-        int pending = cur.seq >= 0 ? claim_next() : total;
+        ChunkUnit cur, nxt;
+        int pending = total;
+        if (warp == 0) {
+            nxt = describe(claim_next());
+            pending = nxt.seq >= 0 ? claim_next() : total;
+        }
         bool ok = true;
         for (int n = 0; ok; ++n) {
-            const int uslot = n % kUnits;
-            if (!mbar_wait(bars + L::B_UEMPTY + uslot, ((n / kUnits) & 1) ^ 1, abort_flag, p.err)) break;
-            if (lane == 0) {
-                unit_ring[uslot] = cur;
-                mbar_arrive(bars + L::B_UFULL + uslot);
+            if (warp == 0) {
+                cur = nxt;
+                const int uslot = n % kUnits;
+                if (!mbar_wait(bars + L::B_UEMPTY + uslot, ((n / kUnits) & 1) ^ 1, abort_flag, p.err)) break;
+                if (lane == 0) {
+                    unit_ring[uslot] = cur;
+                    mbar_arrive(bars + L::B_UFULL + uslot);
+                }
+            } else {
+                cur = claim(n);
             }
             if (cur.seq < 0) break;
             const Keys keys = pair_keys(p, cur.lq, cur.ctx, cur.pair);
             const ChunkTile ta = pair_tile(p, cur, keys, 0), tb = pair_tile(p, cur, keys, 1);
             const int nkv = max(ta.nkv, tb.nkv);
-            const int v0 = cur.part * p.chunk * kKeys;
-            const int vend = keys.p_last - keys.skip + 1;   // virtual keys of the pair
+            const int v0 = cur.part * p.chunk * kKeys + pc * piece;   // this lane's first virtual key
+            const int vend = keys.p_last - keys.skip + 1;             // virtual keys of the pair
             const int32_t* bt = p.block_tables + (size_t)cur.seq * p.max_blocks;
-            // The block id of piece `lane` of key tile j (range-checked where it is used);
+            // The block id of this lane's piece of key tile j (range-checked where it is used);
             // pieces past the last visible key are not looked up.
-            auto load_pieces = [&](int j) {
-                const int v = v0 + j * kKeys + lane * piece;
-                return lane * piece < kKeys && v < vend ? __ldg(bt + (keys.real(v) >> p.block_shift)) : kNoPiece;
+            auto load_piece = [&](int j) {
+                const int v = v0 + j * kKeys;
+                return has_piece && v < vend ? __ldg(bt + (keys.real(v) >> p.block_shift)) : kNoPiece;
             };
-            int cur_blk = load_pieces(0);
-            int nxt_blk = nkv > 1 ? load_pieces(1) : kNoPiece;
-            const ChunkUnit nxt = describe(pending);
-            pending = nxt.seq >= 0 ? claim_next() : total;
+            int cur_blk = load_piece(0);
+            int nxt_blk = nkv > 1 ? load_piece(1) : kNoPiece;
+            if (warp == 0) {
+                nxt = describe(pending);
+                pending = nxt.seq >= 0 ? claim_next() : total;
+            }
             auto load_q = [&](const ChunkTile& t) -> bool {
-                if (t.nkv == 0) return true;
+                if (t.nkv == 0 || warp != 0) return true;
                 const uint32_t qs = qfill % QBUFS;
                 if (!mbar_wait(bars + L::B_QEMPTY + qs, ((qfill / QBUFS) & 1) ^ 1, abort_flag, p.err)) return false;
                 uint8_t* qdst = smem + L::Q_OFF + qs * L::TILE_BYTES;
@@ -483,58 +501,54 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 ++qfill;
                 return true;
             };
-            // K (kv = 0) or V of key tile j, whose block ids the lanes hold.  A block id out of
-            // range is flagged (once, with K) and its rows are zero: their keys score 0 and add 0.
-            auto load_kv = [&](int kv, int j, int blk_lane) -> bool {
+            // This warp's share of K (kv = 0) or V of key tile j.  A block id out of range is
+            // flagged (once, with K) and its rows are zero: their keys score 0 and add 0.
+            auto load_kv = [&](int kv, int j, int blk) -> bool {
                 constexpr int RING = FP8 ? R::STAGES : R::RING;
                 const int slot = fill % RING;
                 uint64_t* full = bars + (FP8 ? L::B_STFULL : L::B_KVFULL) + slot;
                 if (!mbar_wait(bars + (FP8 ? L::B_STEMPTY : L::B_KVEMPTY) + slot, ((fill / RING) & 1) ^ 1,
                                abort_flag, p.err))
                     return false;
-                const bool in_range = blk_lane >= 0 && blk_lane < p.num_blocks;
-                const bool bad = blk_lane != kNoPiece && !in_range;
+                ++fill;
+                const bool in_range = blk >= 0 && blk < p.num_blocks;
+                const bool bad = blk != kNoPiece && !in_range;
                 if (kv == 0 && bad) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
-                const uint32_t valid_mask = __ballot_sync(0xffffffffu, in_range);
-                uint8_t* dst = smem + (FP8 ? L::STAGE_OFF + slot * L::STAGE_BYTES : L::RING_OFF + slot * L::TILE_BYTES);
+                const uint32_t valid = __ballot_sync(0xffffffffu, in_range);
+                uint8_t* tile = smem + (FP8 ? L::STAGE_OFF + slot * L::STAGE_BYTES : L::RING_OFF + slot * L::TILE_BYTES);
                 if constexpr (!FP8) {
-                    const uint32_t bad_mask = __ballot_sync(0xffffffffu, bad);
-                    if (bad_mask != 0) {
-                        for (uint32_t m = bad_mask; m != 0; m &= m - 1) {
-                            const int c = __ffs(m) - 1;
-                            for (int r = 0; r < L::REGIONS; ++r) {
-                                uint4* rows = reinterpret_cast<uint4*>(dst + r * L::REGION_BYTES + c * piece * 128);
-                                for (int k = lane; k < piece * 8; k += 32) rows[k] = make_uint4(0, 0, 0, 0);
-                            }
+                    for (uint32_t m = __ballot_sync(0xffffffffu, bad); m != 0; m &= m - 1) {
+                        const int c = pw + kProducers * (__ffs(m) - 1);
+                        for (int r = 0; r < L::REGIONS; ++r) {
+                            uint4* rows = reinterpret_cast<uint4*>(tile + r * L::REGION_BYTES + c * piece * 128);
+                            for (int k = lane; k < piece * 8; k += 32) rows[k] = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
                 }
                 if (lane == 0) {
-                    if constexpr (FP8) stage_mask[slot] = valid_mask;
-                    mbar_arrive_expect_tx(full, (uint32_t)__popc(valid_mask) *
+                    if constexpr (FP8) stage_mask[slot * kProducers + pw] = valid;
+                    mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) *
                                                     (uint32_t)(FP8 ? piece * (D + 1) : piece * 128 * L::REGIONS));
                 }
-                const CUtensorMap* map = kv ? &v_map : &k_map;
-                for (uint32_t m = valid_mask; m != 0; m &= m - 1) {
-                    const int c = __ffs(m) - 1;
-                    const int blk = __shfl_sync(0xffffffffu, blk_lane, c);
-                    if (lane == 0) {
-                        const int row = keys.real(v0 + j * kKeys + c * piece) & (p.block_size - 1);
-                        const int z = blk * p.block_size + row;
-                        if constexpr (FP8) {
-                            tma_load_3d(dst + c * piece * D, map, full, 0, cur.hk, z);
-                            const uint8_t* sc = (kv ? p.v_scales : p.k_scales) +
-                                                ((size_t)blk * p.hkv + cur.hk) * p.block_size + row;
-                            bulk_load(smem + L::SCALE_OFF + slot * kKeys + c * piece, sc, (uint32_t)piece, full);
-                        } else {
-                            for (int r = 0; r < L::REGIONS; ++r)
-                                tma_load_3d(dst + r * L::REGION_BYTES + c * piece * 128, map, full, r * 64, cur.hk, z);
-                        }
+                __syncwarp();
+                if (in_range) {
+                    const CUtensorMap* map = kv ? &v_map : &k_map;
+                    const int row = keys.real(v0 + j * kKeys) & (p.block_size - 1);
+                    const int z = blk * p.block_size + row;
+                    if constexpr (FP8) {
+                        tma_load_3d(tile + pc * piece * D, map, full, 0, cur.hk, z);
+                        const uint8_t* sc = (kv ? p.v_scales : p.k_scales) +
+                                            ((size_t)blk * p.hkv + cur.hk) * p.block_size + row;
+                        bulk_load(smem + L::SCALE_OFF + slot * kKeys + pc * piece, sc, (uint32_t)piece, full);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < L::REGIONS; ++r)
+                            tma_load_3d(tile + r * L::REGION_BYTES + pc * piece * 128, map, full, r * 64, cur.hk, z);
                     }
                 }
-                ++fill;
+                __syncwarp();
                 return true;
             };
             // K_0 first (its ring slot frees early), then Q_A, V_0, Q_B, then K_j, V_j
@@ -544,11 +558,10 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             if (ok) ok = load_q(tb);
             for (int j = 1; j < nkv && ok; ++j) {
                 cur_blk = nxt_blk;
-                nxt_blk = j + 1 < nkv ? load_pieces(j + 1) : kNoPiece;
+                nxt_blk = j + 1 < nkv ? load_piece(j + 1) : kNoPiece;
                 ok = load_kv(0, j, cur_blk);
                 if (ok) ok = load_kv(1, j, cur_blk);
             }
-            cur = nxt;
         }
         // let every copy this warp started land before the CTA can exit
         if (lane == 0) {
@@ -564,7 +577,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             drain(bars + (FP8 ? L::B_STFULL : L::B_KVFULL), fill, FP8 ? R::STAGES : R::RING);
             drain(bars + L::B_QFULL, qfill, QBUFS);
         }
-      } else if (warp == 1) {
+      } else {
         // ============================ MMA issuer ============================
         const uint32_t IDESC_QK = idesc_bf16_f32(kRows, kKeys, false) | (p.negate_qk ? (1u << 13) : 0u);
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(kRows, D, true);
@@ -859,7 +872,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::SMALL_REGS));
         if constexpr (FP8) {
             const int r = (warp - 12) * 32 + lane;    // key row of the tile
-            const int prow = r / p.piece;             // its piece
+            const int prow = r / p.piece;             // its piece, copied by producer prow % 3
             uint32_t fill = 0;
             bool ok = true;
             for (int n = 0; ok; ++n) {
@@ -876,7 +889,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     }
                     // rows that nobody in the pair sees, or whose block id is bad, become zero
                     const int key = keys.real(v0 + (j >> 1) * kKeys + r);
-                    const bool seen = ((stage_mask[slot] >> prow) & 1) && key <= keys.p_last &&
+                    const bool seen = ((stage_mask[slot * kProducers + prow % kProducers] >> (prow / kProducers)) & 1) && key <= keys.p_last &&
                                       (p.window == 0 || key > keys.p_first - p.window || key < p.sinks);
                     const RowScale f = row_scale(smem[L::SCALE_OFF + slot * kKeys + r]);
                     const uint8_t* src = smem + L::STAGE_OFF + slot * L::STAGE_BYTES + r * D;
