@@ -88,7 +88,7 @@ struct ChunkParams {
     float* lse_out;
     float* o_part;               // [total_q * hq, s_max, D] partial outputs, normalised
     float* lse_part;
-    int4* entries;               // plan: (sequence, pair, partition, partitions of the pair's longer tile)
+    int4* entries;               // plan: (sequence, pair, partition, -)
     int32_t* counter;            // [0] units claimed, [1] entries
     int32_t* nsplit;             // [total_q] partitions of each query token, 0: none
     int32_t* err;
@@ -104,6 +104,50 @@ struct ChunkParams {
     int negate_qk;               // scale < 0: S = -Q K^T
     int out_v8;                  // out is 32-byte aligned
 };
+
+// The virtual keys of a pair of query tiles (see the top): key v is v below `head`, v + skip
+// from there on.
+struct Keys {
+    int p_first, p_last;   // positions of the pair's first and last query token
+    int head, skip;
+    __device__ __forceinline__ int real(int v) const { return v < head ? v : v + skip; }
+    // virtual keys up to position pos
+    __device__ __forceinline__ int upto(int pos) const { return pos + 1 - skip; }
+    __device__ __forceinline__ int tiles(int pos) const { return (pos - skip) / kKeys + 1; }
+};
+__device__ __forceinline__ Keys pair_keys(const ChunkParams& p, int lq, int ctx, int pair) {
+    Keys k;
+    k.p_first = ctx - lq + 2 * pair * p.tq;
+    k.p_last = ctx - lq + min(lq, (2 * pair + 2) * p.tq) - 1;
+    k.head = k.skip = 0;
+    if (p.window > 0) {
+        const int lo = max(0, k.p_first - p.window + 1) / kGran * kGran;
+        k.head = (int)min((long long)lo, ((long long)p.sinks + kGran - 1) / kGran * kGran);
+        k.skip = lo - k.head;
+    }
+    return k;
+}
+// Key tiles that tile x of the pair sees (0: no such tile).
+__device__ __forceinline__ int tile_count(const ChunkParams& p, const Keys& k, int ntok, int x) {
+    return ntok > 0 ? k.tiles(k.p_first + x * p.tq + ntok - 1) : 0;
+}
+__device__ __forceinline__ int tile_tokens(const ChunkParams& p, int lq, int pair, int x) {
+    return min(p.tq, lq - (2 * pair + x) * p.tq);
+}
+
+// A work unit: a pair of query tiles A, B of a sequence, one KV head and one partition of the
+// keys, worked out by the first producer warp for all the others.  seq < 0 ends the loop.
+struct __align__(16) ChunkUnit {
+    int seq, hk, row0, part;   // row0: the pair's first query row
+    int nk[2];                 // key tiles of this partition that A and B see
+    int ntok[2];               // their tokens
+    int ns[2];                 // their partitions
+    int v0;                    // the partition's first virtual key
+    int pad;
+    Keys keys;
+    __device__ __forceinline__ int nkv() const { return max(nk[0], nk[1]); }
+};
+static_assert(sizeof(ChunkUnit) == 64, "unit size");
 
 template <int D, bool FP8>
 struct ChunkLayout {
@@ -126,59 +170,11 @@ struct ChunkLayout {
     static constexpr int NBARS = B_STEMPTY + R::STAGES;
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;     // tmem base, abort flag, staged piece masks
     static constexpr int UNIT_OFF = (MISC_OFF + 8 + 4 * kProducers * R::STAGES + 15) / 16 * 16;
-    static constexpr int BYTES = UNIT_OFF + 32 * kUnits;
+    static constexpr int BYTES = UNIT_OFF + (int)sizeof(ChunkUnit) * kUnits;
     static constexpr int ALLOC = BYTES + 1024;               // room to align the base to 1024
 };
 static_assert(ChunkLayout<128, false>::ALLOC <= 227 * 1024 && ChunkLayout<128, true>::ALLOC <= 227 * 1024,
               "shared memory per CTA");
-
-// A work unit: the pair of query tiles (2 pair, 2 pair + 1) of a sequence, one KV head and one
-// partition of the keys.  seq < 0 ends the loop.
-struct ChunkUnit {
-    int seq, pair, part, ns;
-    int hk, q0, lq, ctx;
-};
-static_assert(sizeof(ChunkUnit) == 32, "unit size");
-
-// The virtual keys of a pair (see the top): key v is v below `head`, v + skip from there on.
-struct Keys {
-    int p_first, p_last;   // positions of the pair's first and last query token
-    int head, skip;
-    int tiles;             // 128-key tiles of the whole range
-    __device__ __forceinline__ int real(int v) const { return v < head ? v : v + skip; }
-};
-__device__ __forceinline__ Keys pair_keys(const ChunkParams& p, int lq, int ctx, int pair) {
-    Keys k;
-    k.p_first = ctx - lq + 2 * pair * p.tq;
-    k.p_last = ctx - lq + min(lq, (2 * pair + 2) * p.tq) - 1;
-    k.head = k.skip = 0;
-    if (p.window > 0) {
-        const int lo = max(0, k.p_first - p.window + 1) / kGran * kGran;
-        const int hs = (int)min((long long)lo, ((long long)p.sinks + kGran - 1) / kGran * kGran);
-        k.head = hs;
-        k.skip = lo - hs;
-    }
-    k.tiles = (k.p_last - k.skip) / kKeys + 1;
-    return k;
-}
-
-struct ChunkTile {
-    bool valid;
-    int tok0, ntok;    // its tokens in the chunk
-    int nkv;           // key tiles of this partition that it sees
-    int ns;            // partitions it has
-};
-// Tile A (x = 0) or B (x = 1) of unit u.
-__device__ __forceinline__ ChunkTile pair_tile(const ChunkParams& p, const ChunkUnit& u, const Keys& k, int x) {
-    ChunkTile t;
-    t.tok0 = (2 * u.pair + x) * p.tq;
-    t.ntok = min(p.tq, u.lq - t.tok0);
-    t.valid = t.ntok > 0;
-    const int n = t.valid ? (u.ctx - u.lq + t.tok0 + t.ntok - 1 - k.skip) / kKeys + 1 : 0;
-    t.nkv = max(0, min(p.chunk, n - u.part * p.chunk));
-    t.ns = (n + p.chunk - 1) / p.chunk;
-    return t;
-}
 
 // ------------------------------------------------------------------------------------
 // plan: the units, those with the most key tiles first
@@ -211,7 +207,11 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const ChunkParams p) {
         const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= p.total_q && r.lq <= p.max_q && r.ctx >= r.lq &&
                         r.ctx <= lim;
         if (!ok && flag && r.w == 0) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
-        r.tiles = ok && 2 * r.w * p.tq < r.lq ? pair_keys(p, r.lq, r.ctx, r.w).tiles : 0;
+        r.tiles = 0;
+        if (ok && 2 * r.w * p.tq < r.lq) {
+            const Keys k = pair_keys(p, r.lq, r.ctx, r.w);
+            r.tiles = k.tiles(k.p_last);
+        }
         return r;
     };
     // descending order: bucket of a unit with n key tiles
@@ -243,11 +243,10 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const ChunkParams p) {
         const Pair r = pair(i, false);
         if (r.tiles == 0) continue;
         const int full = r.tiles / p.chunk, rest = r.tiles - full * p.chunk;
-        const int ns = full + (rest > 0);
         // (cumulative lengths that run backwards can claim rows twice, and so more entries
         // than the table holds: what does not fit is dropped and flagged below)
         auto put = [&](int pos, int s) {
-            if (pos < p.max_entries) p.entries[pos] = make_int4(r.b, r.w, s, ns);
+            if (pos < p.max_entries) p.entries[pos] = make_int4(r.b, r.w, s, 0);
         };
         if (full > 0) {
             const int pos = atomicAdd(&s_hist[bucket(p.chunk)], full);
@@ -255,11 +254,11 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const ChunkParams p) {
         }
         if (rest > 0) put(atomicAdd(&s_hist[bucket(rest)], 1), full);
         if (p.s_max > 1) {
-            const ChunkUnit u{r.b, r.w, 0, ns, 0, r.q0, r.lq, r.ctx};
             const Keys k = pair_keys(p, r.lq, r.ctx, r.w);
             for (int x = 0; x < 2; ++x) {
-                const ChunkTile t = pair_tile(p, u, k, x);
-                for (int j = 0; j < t.ntok; ++j) p.nsplit[r.q0 + t.tok0 + j] = t.ns;
+                const int ntok = tile_tokens(p, r.lq, r.w, x);
+                const int parts = (tile_count(p, k, ntok, x) + p.chunk - 1) / p.chunk;
+                for (int j = 0; j < ntok; ++j) p.nsplit[r.q0 + (2 * r.w + x) * p.tq + j] = parts;
             }
         }
     }
@@ -407,8 +406,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         const int slot = n % kUnits;
         ChunkUnit u;
         if (!mbar_wait(bars + L::B_UFULL + slot, (n / kUnits) & 1, abort_flag, p.err)) {
+            u = ChunkUnit{};
             u.seq = -2;
-            u.pair = u.part = u.ns = u.hk = u.q0 = u.lq = u.ctx = 0;
             return u;
         }
         u = unit_ring[slot];
@@ -434,17 +433,24 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         auto claim_next = [&]() -> int { return lane == 0 ? atomicAdd(p.counter, 1) : 0; };
         auto describe = [&](int pending) -> ChunkUnit {
             const int i = __shfl_sync(0xffffffffu, pending, 0);
-            ChunkUnit u{-1, 0, 0, 0, 0, 0, 0, 0};
+            ChunkUnit u{};
+            u.seq = -1;
             if (i < total) {
                 const int4 e = __ldcg(p.entries + i / p.hkv);
+                const int q0 = __ldg(p.cu_q + e.x), lq = __ldg(p.cu_q + e.x + 1) - q0;
                 u.seq = e.x;
-                u.pair = e.y;
-                u.part = e.z;
-                u.ns = e.w;
                 u.hk = i % p.hkv;
-                u.q0 = __ldg(p.cu_q + e.x);
-                u.lq = __ldg(p.cu_q + e.x + 1) - u.q0;
-                u.ctx = __ldg(p.context_lens + e.x);
+                u.row0 = q0 + 2 * e.y * p.tq;
+                u.part = e.z;
+                u.v0 = e.z * p.chunk * kKeys;
+                u.keys = pair_keys(p, lq, __ldg(p.context_lens + e.x), e.y);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    u.ntok[x] = tile_tokens(p, lq, e.y, x);
+                    const int n = tile_count(p, u.keys, u.ntok[x], x);
+                    u.nk[x] = max(0, min(p.chunk, n - e.z * p.chunk));
+                    u.ns[x] = (n + p.chunk - 1) / p.chunk;
+                }
             }
             return u;
         };
@@ -468,11 +474,10 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 cur = claim(n);
             }
             if (cur.seq < 0) break;
-            const Keys keys = pair_keys(p, cur.lq, cur.ctx, cur.pair);
-            const ChunkTile ta = pair_tile(p, cur, keys, 0), tb = pair_tile(p, cur, keys, 1);
-            const int nkv = max(ta.nkv, tb.nkv);
-            const int v0 = cur.part * p.chunk * kKeys + pc * piece;   // this lane's first virtual key
-            const int vend = keys.p_last - keys.skip + 1;             // virtual keys of the pair
+            const Keys keys = cur.keys;
+            const int nkv = cur.nkv();
+            const int v0 = cur.v0 + pc * piece;             // this lane's first virtual key
+            const int vend = keys.upto(keys.p_last);        // virtual keys of the pair
             const int32_t* bt = p.block_tables + (size_t)cur.seq * p.max_blocks;
             // The block id of this lane's piece of key tile j (range-checked where it is used);
             // pieces past the last visible key are not looked up.
@@ -486,8 +491,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 nxt = describe(pending);
                 pending = nxt.seq >= 0 ? claim_next() : total;
             }
-            auto load_q = [&](const ChunkTile& t) -> bool {
-                if (t.nkv == 0 || warp != 0) return true;
+            auto load_q = [&](int x) -> bool {
+                if ((x ? cur.nk[1] : cur.nk[0]) == 0 || warp != 0) return true;
                 const uint32_t qs = qfill % QBUFS;
                 if (!mbar_wait(bars + L::B_QEMPTY + qs, ((qfill / QBUFS) & 1) ^ 1, abort_flag, p.err)) return false;
                 uint8_t* qdst = smem + L::Q_OFF + qs * L::TILE_BYTES;
@@ -496,7 +501,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     mbar_arrive_expect_tx(bars + L::B_QFULL + qs, (uint32_t)(p.tq * p.group * 128 * L::REGIONS));
                     for (int r = 0; r < L::REGIONS; ++r)
                         tma_load_3d(qdst + r * L::REGION_BYTES, &q_map, bars + L::B_QFULL + qs, r * 64,
-                                    cur.hk * p.group, cur.q0 + t.tok0);
+                                    cur.hk * p.group, cur.row0 + x * p.tq);
                 }
                 ++qfill;
                 return true;
@@ -553,9 +558,9 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             };
             // K_0 first (its ring slot frees early), then Q_A, V_0, Q_B, then K_j, V_j
             ok = load_kv(0, 0, cur_blk);
-            if (ok) ok = load_q(ta);
+            if (ok) ok = load_q(0);
             if (ok) ok = load_kv(1, 0, cur_blk);
-            if (ok) ok = load_q(tb);
+            if (ok) ok = load_q(1);
             for (int j = 1; j < nkv && ok; ++j) {
                 cur_blk = nxt_blk;
                 nxt_blk = j + 1 < nkv ? load_piece(j + 1) : kNoPiece;
@@ -612,11 +617,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         for (int n = 0; ok; ++n) {
             const ChunkUnit u = claim(n);
             if (__shfl_sync(0xffffffffu, u.seq, 0) < 0) break;
-            const Keys keys = pair_keys(p, u.lq, u.ctx, u.pair);
-            const ChunkTile ta = pair_tile(p, u, keys, 0), tb = pair_tile(p, u, keys, 1);
-            const int nk[2] = {__shfl_sync(0xffffffffu, ta.nkv, 0), __shfl_sync(0xffffffffu, tb.nkv, 0)};
+            const int nk[2] = {__shfl_sync(0xffffffffu, u.nk[0], 0), __shfl_sync(0xffffffffu, u.nk[1], 0)};
             const int nkv = max(nk[0], nk[1]);
-            const int v0 = u.part * p.chunk * kKeys;
             // S of key tile 0: tile A as soon as Q_A and K_0 are in, then tile B
             if (!mbar_wait(bars + L::B_KVFULL + fbase % R::RING, (fbase / R::RING) & 1, abort_flag, p.err)) break;
             uint32_t qsl[2] = {0, 0};
@@ -644,27 +646,6 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 if (!mbar_wait(bars + L::B_KVFULL + vslot, (fv / R::RING) & 1, abort_flag, p.err)) {
                     ok = false;
                     break;
-                }
-                if constexpr (!FP8) {
-                    // zero the V rows that no row of the pair sees (stale cache rows, or never
-                    // loaded); the virtual range has such rows behind its end, and with a window
-                    // between the sinks and the first row's window
-                    const int base = v0 + j * kKeys;
-                    const int seen_a = p.window > 0 ? min(p.sinks, keys.p_first + 1) : 0;
-                    const int seen_b = p.window > 0 ? max(0, keys.p_first - p.window + 1) - keys.skip : 0;
-                    const int seen_c = keys.p_last + 1 - keys.skip;
-                    if (base + kKeys > seen_c || (base < seen_b && base + kKeys > seen_a)) {
-                        uint8_t* vt = smem + L::RING_OFF + vslot * L::TILE_BYTES;
-                        for (int r = 0; r < kKeys; ++r) {
-                            const int v = base + r;
-                            if (v < seen_c && (v >= seen_b || v < seen_a)) continue;
-                            if (lane < 8 * L::REGIONS)
-                                *reinterpret_cast<uint4*>(vt + (lane >> 3) * L::REGION_BYTES + r * 128 +
-                                                          (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
                 }
                 bool k_next = false;
                 for (int x = 0; x < 2; ++x) {
@@ -738,37 +719,42 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         uint64_t* b_odone = bars + L::B_ODONE + x;
         uint64_t* b_ofinal = bars + L::B_OFINAL + x;
         uint64_t* b_ofree = bars + L::B_OFREE + x;
-        uint32_t s_use = 0;
+        uint32_t s_use = 0, fbase = 0;
         int tcount = 0;
         uint32_t pv_before = 0;                       // PVs issued for this tile slot before
         for (int n = 0;; ++n) {
             const ChunkUnit u = claim(n);
             if (u.seq < 0) break;
-            const Keys keys = pair_keys(p, u.lq, u.ctx, u.pair);
-            const ChunkTile t = pair_tile(p, u, keys, x);
-            if (t.nkv == 0) continue;
+            const uint32_t vfill = fbase + 1;   // ring position of V_0
+            fbase += 2 * (uint32_t)u.nkv();
+            const int nk = x ? u.nk[1] : u.nk[0], ntok = x ? u.ntok[1] : u.ntok[0];   // (no indexed copy)
+            if (nk == 0) continue;
+            const Keys& keys = u.keys;
             // a warp whose rows are all behind the tile's last one only keeps the protocol
-            const bool idle = quarter * 32 >= t.ntok * p.group;
-            const int pos = u.ctx - u.lq + t.tok0 + min(rtok, t.ntok - 1);
+            const bool idle = quarter * 32 >= ntok * p.group;
+            const int pos = keys.p_first + x * p.tq + min(rtok, ntok - 1);
             // virtual keys that the row sees: [0, va) and [vb, vc)
             const int va = p.window > 0 ? min(p.sinks, pos + 1) : 0;
             const int vb = p.window > 0 ? max(0, pos - p.window + 1) - keys.skip : 0;
-            const int vc = pos + 1 - keys.skip;
+            const int vc = keys.upto(pos);
+            // and that some row of the pair sees: [0, pa) and [pb, pc)
+            const int pa = p.window > 0 ? min(p.sinks, keys.p_first + 1) : 0;
+            const int pb = p.window > 0 ? max(0, keys.p_first - p.window + 1) - keys.skip : 0;
+            const int pc = keys.upto(keys.p_last);
             const int a_min = __reduce_min_sync(0xffffffffu, va);
             const int b_max = __reduce_max_sync(0xffffffffu, vb);
             const int c_min = __reduce_min_sync(0xffffffffu, vc);
-            const int v0 = u.part * p.chunk * kKeys;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            for (int j = 0; j < t.nkv; ++j) {
+            for (int j = 0; j < nk; ++j) {
                 if (!mbar_wait(b_sfull, s_use & 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
                 ++s_use;
                 tc_fence_after();
+                const int base = u.v0 + j * kKeys;
                 if (!idle) {
-                    const int base = v0 + j * kKeys;
                     // no mask anywhere in the warp
                     const bool open = base + kKeys <= c_min && (base >= b_max || base + kKeys <= a_min);
                     uint32_t sv[kKeys];
@@ -809,6 +795,27 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     }
                     tmem_wait_st();
                 }
+                if constexpr (!FP8) {
+                    // V rows that nobody in the pair sees hold stale values, or what the ring
+                    // held before: zeroed here, a row per thread, by the warps of the first tile
+                    // whose P V reads them (the widening does it for the e4m3 cache)
+                    if ((base + kKeys > pc || (base < pb && base + kKeys > pa)) && (x == 0 || j >= u.nk[0])) {
+                        const uint32_t fv = vfill + 2 * (uint32_t)j;
+                        if (!mbar_wait(bars + L::B_KVFULL + fv % R::RING, (fv / R::RING) & 1, abort_flag, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        const int v = base + r;
+                        if (!(v < pc && (v >= pb || v < pa))) {
+                            uint8_t* row = smem + L::RING_OFF + (fv % R::RING) * L::TILE_BYTES + r * 128;
+#pragma unroll
+                            for (int c = 0; c < 8 * L::REGIONS; ++c)   // (r & 7: a warp's stores spread over the banks)
+                                *reinterpret_cast<uint4*>(row + (c >> 3) * L::REGION_BYTES + (((c ^ r) & 7) << 4)) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_pfull);
@@ -816,12 +823,12 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             if (!ok) break;
             if (!mbar_wait(b_ofinal, tcount & 1, abort_flag, p.err)) break;
             tc_fence_after();
-            const bool row_ok = rtok < t.ntok;
+            const bool row_ok = rtok < ntok;
             // (a sum that is not a number keeps the row from looking empty)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            const size_t orow = (size_t)(u.q0 + t.tok0 + rtok) * p.hq + u.hk * p.group + rhead;
-            const bool partial = t.ns > 1;
+            const size_t orow = (size_t)(u.row0 + x * p.tq + rtok) * p.hq + u.hk * p.group + rhead;
+            const bool partial = (x ? u.ns[1] : u.ns[0]) > 1;
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
             float* pdst = p.o_part + (orow * p.s_max + u.part) * D;
 #pragma unroll
@@ -864,7 +871,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 if (partial) __stcg(p.lse_part + orow * p.s_max + u.part, lse);
                 else if (p.lse_out != nullptr) p.lse_out[orow] = lse;
             }
-            pv_before += (uint32_t)t.nkv;
+            pv_before += (uint32_t)nk;
             ++tcount;
         }
     } else {
@@ -878,9 +885,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             for (int n = 0; ok; ++n) {
                 const ChunkUnit u = claim(n);
                 if (u.seq < 0) break;
-                const Keys keys = pair_keys(p, u.lq, u.ctx, u.pair);
-                const int nkv = max(pair_tile(p, u, keys, 0).nkv, pair_tile(p, u, keys, 1).nkv);
-                const int v0 = u.part * p.chunk * kKeys;
+                const Keys keys = u.keys;
+                const int nkv = u.nkv();
                 for (int j = 0; j < 2 * nkv && ok; ++j, ++fill) {   // K_0, V_0, K_1, ...
                     const int slot = fill % R::STAGES, ring = fill % R::RING;
                     if (!mbar_wait(bars + L::B_STFULL + slot, (fill / R::STAGES) & 1, abort_flag, p.err)) {
@@ -888,7 +894,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                         break;
                     }
                     // rows that nobody in the pair sees, or whose block id is bad, become zero
-                    const int key = keys.real(v0 + (j >> 1) * kKeys + r);
+                    const int key = keys.real(u.v0 + (j >> 1) * kKeys + r);
                     const bool seen = ((stage_mask[slot * kProducers + prow % kProducers] >> (prow / kProducers)) & 1) && key <= keys.p_last &&
                                       (p.window == 0 || key > keys.p_first - p.window || key < p.sinks);
                     const RowScale f = row_scale(smem[L::SCALE_OFF + slot * kKeys + r]);
