@@ -783,7 +783,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                             break;
                         }
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
                             tmem_ld32(o_col + c * 32, o);
@@ -831,7 +831,9 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const bool partial = (x ? u.ns[1] : u.ns[0]) > 1;
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
             float* pdst = p.o_part + (orow * p.s_max + u.part) * D;
-#pragma unroll
+            // (loops stay rolled where they can: the warps of a sub-partition share its instruction
+            // cache, and a unit's boundary is code that runs once in many key tiles)
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(o_col + c * 32, o);
@@ -901,12 +903,6 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     const uint8_t* src = smem + L::STAGE_OFF + slot * L::STAGE_BYTES + r * D;
                     // 128-byte rows: chunk c lies at c ^ (r % 8); 64-byte rows: at c ^ (r / 2 % 4)
                     const int sx = D == 128 ? r & 7 : (r >> 1) & 3;
-                    uint4 code[D / 16];
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c)
-                        code[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sx) << 4));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + L::B_STEMPTY + slot);   // the codes are in registers
                     if (!mbar_wait(bars + L::B_KVEMPTY + ring, ((fill / R::RING) & 1) ^ 1, abort_flag, p.err)) {
                         ok = false;
                         break;
@@ -918,24 +914,34 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                         *reinterpret_cast<uint4*>(d + ((((c % 4) * 2 + 1) ^ (r & 7)) << 4)) = hi;
                     };
                     if (__all_sync(0xffffffffu, seen && f.half != 0)) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D / 16; c0 += 4) {
+                            uint4 code[4];
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint4 lo, hi;
-                            widen16(code[c], f.half, lo, hi);
-                            put(c, lo, hi);
+                            for (int i = 0; i < 4; ++i)
+                                code[i] = *reinterpret_cast<const uint4*>(src + (((c0 + i) ^ sx) << 4));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint4 lo, hi;
+                                widen16(code[i], f.half, lo, hi);
+                                put(c0 + i, lo, hi);
+                            }
                         }
                     } else {   // a warp with a special row
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint4 lo, hi;
-                            widen16_any(code[c], f.value, lo, hi);
+                            widen16_any(*reinterpret_cast<const uint4*>(src + ((c ^ sx) << 4)), f.value, lo, hi);
                             if (!seen) lo = hi = make_uint4(0, 0, 0, 0);
                             put(c, lo, hi);
                         }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + L::B_KVFULL + ring);
+                    if (lane == 0) {
+                        mbar_arrive(bars + L::B_STEMPTY + slot);
+                        mbar_arrive(bars + L::B_KVFULL + ring);
+                    }
                 }
             }
         }
