@@ -474,9 +474,10 @@ nvpa_status_t nvpa_paged_decode_attention_window(
 }
 
 // Which kernel a chunk call takes: up to kRowKernelRows query rows per KV head (tokens times
-// heads of its group) go to the row kernel, which reads the keys once for 16 rows; more go to
-// the 128-row tiles.
-constexpr int kRowKernelRows = 16;
+// heads of its group) go to the row kernel, which reads the keys once for 24 rows; more go to
+// the 128-row tiles.  (8 contexts of 8 k keys in 8 bits, 32 / 8 heads: 20 rows 65 us by rows,
+// 91 by tiles; 32 rows 106 and 92.)
+constexpr int kRowKernelRows = 24;
 static bool chunk_on_tiles(int max_seqlen_q, int num_q_heads, int num_kv_heads) {
     return (long long)max_seqlen_q * (num_q_heads / num_kv_heads) > kRowKernelRows;
 }

@@ -231,9 +231,9 @@ __device__ __forceinline__ float max_over_keys(float v) {   // lanes with the sa
 }
 
 // A stage of a warp's ring: TILES 16-key tiles that are worked on together.
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 struct RowStage {
-    static constexpr int TILES = FP8 ? 2 : 1;
+    static constexpr int TILES = FP8 && NT <= 2 ? 2 : 1;
     static constexpr int ROW = FP8 ? D : 2 * D;             // bytes of a key's row
     static constexpr int CHUNKS = ROW / 16;
     static constexpr int KV = kTileKeys * ROW;              // K of a tile, then its V
@@ -252,7 +252,7 @@ constexpr int kRowStages = 2;
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kRowWarps * 32)
 row_attention_kernel(const RowParams p) {
-    using Stage = RowStage<D, FP8>;
+    using Stage = RowStage<D, FP8, NT>;
     constexpr int STAGES = kRowStages;
     constexpr int TILES = Stage::TILES;
     constexpr uint32_t ALL = TILES == 2 ? 0xffffffffu : 0xffffu;   // every key of a stage
@@ -776,9 +776,9 @@ row_attention_kernel(const RowParams p) {
 // ------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 constexpr int row_smem() {
-    return kRowWarps * kRowStages * (RowStage<D, FP8>::BYTES + 48);
+    return kRowWarps * kRowStages * (RowStage<D, FP8, NT>::BYTES + 48);
 }
 
 template <int D, bool FP8, int NT>
@@ -789,7 +789,7 @@ cudaError_t launch_rows(const RowParams& p, long long max_items, cudaStream_t st
     cudaGetDevice(&dev);
     dev &= 63;
     auto kern = row_attention_kernel<D, FP8, NT>;
-    constexpr int smem = row_smem<D, FP8>();
+    constexpr int smem = row_smem<D, FP8, NT>();
     std::call_once(once[dev], [&] {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         int n = 0;
@@ -845,7 +845,7 @@ RowGeometry row_geometry(int batch, int total_q, int max_q, int hq, int hkv, int
                          int window, int sinks, int num_splits) {
     RowGeometry r{};
     const int group = std::max(1, hq / hkv);
-    r.nt = max_q * group <= 8 ? 1 : 2;
+    r.nt = max_q * group <= 8 ? 1 : max_q * group <= 16 ? 2 : 3;
     r.tok = std::max(1, std::min(max_q, 8 * r.nt / group));
     r.row_tiles = std::max(1, (max_q + r.tok - 1) / r.tok);
     r.tiles = std::min((long long)batch * r.row_tiles, (long long)batch + total_q / r.tok);
@@ -936,6 +936,7 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     if (c.head_dim == DD && fp8 == FF && r.nt == NN) e = launch_rows<DD, FF, NN>(p, max_items, stream);
     NVPA_CASE(128, false, 1) NVPA_CASE(128, false, 2) NVPA_CASE(128, true, 1) NVPA_CASE(128, true, 2)
     NVPA_CASE(64, false, 1) NVPA_CASE(64, false, 2) NVPA_CASE(64, true, 1) NVPA_CASE(64, true, 2)
+    NVPA_CASE(128, false, 3) NVPA_CASE(128, true, 3) NVPA_CASE(64, false, 3) NVPA_CASE(64, true, 3)
 #undef NVPA_CASE
     if (e != cudaSuccess) return cuda_failure(e, "row attention launch");
     if (r.s_max > 1) {
