@@ -88,7 +88,7 @@ struct ChunkParams {
     float* lse_out;
     float* o_part;               // [total_q * hq, s_max, D] partial outputs, normalised
     float* lse_part;
-    int4* entries;               // plan: (sequence, pair, partition, -)
+    int4* entries;               // plan: (sequence, pair, unit of the pair's keys, -)
     int32_t* counter;            // [0] units claimed, [1] entries
     int32_t* nsplit;             // [total_q] partitions of each query token, 0: none
     int32_t* err;
@@ -99,6 +99,9 @@ struct ChunkParams {
     int piece;                   // rows per K/V copy
     int window, sinks;           // window 0: none
     int chunk;                   // key tiles per partition
+    int split;                   // chunks of one query tile: tiles A and B are two partitions of it
+    int b_step;                  // tokens between tiles A and B: tq, split: 0
+    int unit_tiles;              // key tiles per unit: chunk, split: 2 chunk
     int s_max, max_entries;
     float scale_log2;            // > 0
     int negate_qk;               // scale < 0: S = -Q K^T
@@ -135,17 +138,46 @@ __device__ __forceinline__ int tile_tokens(const ChunkParams& p, int lq, int pai
     return min(p.tq, lq - (2 * pair + x) * p.tq);
 }
 
+// The order in which a unit's K/V tiles pass through the rings, walked by every role: K_0 of
+// each stream, then for each key tile j and stream x: V_xj, K_x(j+1).
+struct TileWalk {
+    int x = 0, kv = 0, j = 0;
+    __device__ __forceinline__ void next(int sn0, int sn1) {
+        if (kv == 1 && j + 1 < (x ? sn1 : sn0)) {   // V_xj -> K_x(j+1)
+            kv = 0;
+            ++j;
+            return;
+        }
+        if (kv == 0 && j == 0) {                    // the K_0s -> V_00
+            if (x == 0 && sn1 > 0) x = 1;
+            else x = 0, kv = 1;
+            return;
+        }
+        const int round = kv ? j : j - 1;           // stream x is done with it
+        kv = 1;
+        if (x == 0 && round < sn1) {
+            x = 1;
+            j = round;
+        } else {
+            x = 0;
+            j = round + 1;
+        }
+    }
+};
+
 // A work unit: a pair of query tiles A, B of a sequence, one KV head and one partition of the
 // keys, worked out by the first producer warp for all the others.  seq < 0 ends the loop.
 struct __align__(16) ChunkUnit {
-    int seq, hk, row0, part;   // row0: the pair's first query row
-    int nk[2];                 // key tiles of this partition that A and B see
+    int seq, hk, row0, part;   // row0: the first query row; part: partition of A (B: + split)
+    int nk[2];                 // key tiles of their partition that A and B see
     int ntok[2];               // their tokens
     int ns[2];                 // their partitions
-    int v0;                    // the partition's first virtual key
-    int pad;
+    int sn[2];                 // K/V tiles that the unit reads: one stream of the longer tile's
+                               // key tiles; split: a stream for A and one for B
     Keys keys;
-    __device__ __forceinline__ int nkv() const { return max(nk[0], nk[1]); }
+    __device__ __forceinline__ int first_key(const ChunkParams& p, int x) const {   // virtual, of stream x
+        return (part * p.chunk + (x && p.split ? p.chunk : 0)) * kKeys;
+    }
 };
 static_assert(sizeof(ChunkUnit) == 64, "unit size");
 
@@ -220,8 +252,8 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const ChunkParams p) {
     for (int i = tid; i < n; i += blockDim.x) {
         const Pair r = pair(i, true);
         if (r.tiles == 0) continue;
-        const int full = r.tiles / p.chunk, rest = r.tiles - full * p.chunk;
-        if (full > 0) atomicAdd(&s_hist[bucket(p.chunk)], full);
+        const int full = r.tiles / p.unit_tiles, rest = r.tiles - full * p.unit_tiles;
+        if (full > 0) atomicAdd(&s_hist[bucket(p.unit_tiles)], full);
         if (rest > 0) atomicAdd(&s_hist[bucket(rest)], 1);
     }
     __syncthreads();
@@ -242,14 +274,14 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const ChunkParams p) {
     for (int i = tid; i < n; i += blockDim.x) {
         const Pair r = pair(i, false);
         if (r.tiles == 0) continue;
-        const int full = r.tiles / p.chunk, rest = r.tiles - full * p.chunk;
+        const int full = r.tiles / p.unit_tiles, rest = r.tiles - full * p.unit_tiles;
         // (cumulative lengths that run backwards can claim rows twice, and so more entries
         // than the table holds: what does not fit is dropped and flagged below)
         auto put = [&](int pos, int s) {
             if (pos < p.max_entries) p.entries[pos] = make_int4(r.b, r.w, s, 0);
         };
         if (full > 0) {
-            const int pos = atomicAdd(&s_hist[bucket(p.chunk)], full);
+            const int pos = atomicAdd(&s_hist[bucket(p.unit_tiles)], full);
             for (int s = 0; s < full; ++s) put(pos + s, s);
         }
         if (rest > 0) put(atomicAdd(&s_hist[bucket(rest)], 1), full);
@@ -441,16 +473,17 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 u.seq = e.x;
                 u.hk = i % p.hkv;
                 u.row0 = q0 + 2 * e.y * p.tq;
-                u.part = e.z;
-                u.v0 = e.z * p.chunk * kKeys;
+                u.part = p.split ? 2 * e.z : e.z;
                 u.keys = pair_keys(p, lq, __ldg(p.context_lens + e.x), e.y);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    u.ntok[x] = tile_tokens(p, lq, e.y, x);
-                    const int n = tile_count(p, u.keys, u.ntok[x], x);
-                    u.nk[x] = max(0, min(p.chunk, n - e.z * p.chunk));
+                    u.ntok[x] = tile_tokens(p, lq, e.y, p.split ? 0 : x);
+                    const int n = tile_count(p, u.keys, u.ntok[x], p.split ? 0 : x);
+                    u.nk[x] = max(0, min(p.chunk, n - u.first_key(p, x) / kKeys));
                     u.ns[x] = (n + p.chunk - 1) / p.chunk;
                 }
+                u.sn[0] = p.split ? u.nk[0] : max(u.nk[0], u.nk[1]);
+                u.sn[1] = p.split ? u.nk[1] : 0;
             }
             return u;
         };
@@ -475,24 +508,26 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             }
             if (cur.seq < 0) break;
             const Keys keys = cur.keys;
-            const int nkv = cur.nkv();
-            const int v0 = cur.v0 + pc * piece;             // this lane's first virtual key
-            const int vend = keys.upto(keys.p_last);        // virtual keys of the pair
+            const int sn0 = cur.sn[0], sn1 = cur.sn[1];
+            const int va0 = cur.first_key(p, 0) + pc * piece, vb0 = cur.first_key(p, 1) + pc * piece;
+            const int vend = keys.upto(keys.p_last);        // virtual keys of the unit's rows
             const int32_t* bt = p.block_tables + (size_t)cur.seq * p.max_blocks;
-            // The block id of this lane's piece of key tile j (range-checked where it is used);
-            // pieces past the last visible key are not looked up.
-            auto load_piece = [&](int j) {
-                const int v = v0 + j * kKeys;
-                return has_piece && v < vend ? __ldg(bt + (keys.real(v) >> p.block_shift)) : kNoPiece;
+            // The block id of this lane's piece of key tile j of stream x (range-checked where it
+            // is used); pieces past the last visible key are not looked up.
+            auto load_piece = [&](int x, int j) {
+                const int v = (x ? vb0 : va0) + j * kKeys;
+                return has_piece && j < (x ? sn1 : sn0) && v < vend ? __ldg(bt + (keys.real(v) >> p.block_shift))
+                                                                    : kNoPiece;
             };
-            int cur_blk = load_piece(0);
-            int nxt_blk = nkv > 1 ? load_piece(1) : kNoPiece;
+            // of each stream's current key tile and the next
+            int blk_a = load_piece(0, 0), next_a = load_piece(0, 1);
+            int blk_b = load_piece(1, 0), next_b = load_piece(1, 1);
             if (warp == 0) {
                 nxt = describe(pending);
                 pending = nxt.seq >= 0 ? claim_next() : total;
             }
             auto load_q = [&](int x) -> bool {
-                if ((x ? cur.nk[1] : cur.nk[0]) == 0 || warp != 0) return true;
+                if ((x ? p.split || cur.nk[1] == 0 : cur.nk[0] == 0) || warp != 0) return true;
                 const uint32_t qs = qfill % QBUFS;
                 if (!mbar_wait(bars + L::B_QEMPTY + qs, ((qfill / QBUFS) & 1) ^ 1, abort_flag, p.err)) return false;
                 uint8_t* qdst = smem + L::Q_OFF + qs * L::TILE_BYTES;
@@ -508,7 +543,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             };
             // This warp's share of K (kv = 0) or V of key tile j.  A block id out of range is
             // flagged (once, with K) and its rows are zero: their keys score 0 and add 0.
-            auto load_kv = [&](int kv, int j, int blk) -> bool {
+            auto load_kv = [&](int x, int kv, int j, int blk) -> bool {
                 constexpr int RING = FP8 ? R::STAGES : R::RING;
                 const int slot = fill % RING;
                 uint64_t* full = bars + (FP8 ? L::B_STFULL : L::B_KVFULL) + slot;
@@ -540,7 +575,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 __syncwarp();
                 if (in_range) {
                     const CUtensorMap* map = kv ? &v_map : &k_map;
-                    const int row = keys.real(v0 + j * kKeys) & (p.block_size - 1);
+                    const int row = keys.real((x ? vb0 : va0) + j * kKeys) & (p.block_size - 1);
                     const int z = blk * p.block_size + row;
                     if constexpr (FP8) {
                         tma_load_3d(tile + pc * piece * D, map, full, 0, cur.hk, z);
@@ -556,16 +591,20 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 __syncwarp();
                 return true;
             };
-            // K_0 first (its ring slot frees early), then Q_A, V_0, Q_B, then K_j, V_j
-            ok = load_kv(0, 0, cur_blk);
-            if (ok) ok = load_q(0);
-            if (ok) ok = load_kv(1, 0, cur_blk);
-            if (ok) ok = load_q(1);
-            for (int j = 1; j < nkv && ok; ++j) {
-                cur_blk = nxt_blk;
-                nxt_blk = j + 1 < nkv ? load_piece(j + 1) : kNoPiece;
-                ok = load_kv(0, j, cur_blk);
-                if (ok) ok = load_kv(1, j, cur_blk);
+            // K_0 first (its ring slot frees early), then Q_A, ..., V_0, Q_B, and the rest
+            TileWalk w;
+            for (int i = 0; i < 2 * (sn0 + sn1) && ok; ++i, w.next(sn0, sn1)) {
+                if (w.kv == 0 && w.j > 0) {   // on to the stream's next key tile
+                    if (w.x) {
+                        blk_b = next_b;
+                        next_b = load_piece(1, w.j + 1);
+                    } else {
+                        blk_a = next_a;
+                        next_a = load_piece(0, w.j + 1);
+                    }
+                }
+                ok = load_kv(w.x, w.kv, w.j, w.x ? blk_b : blk_a);
+                if (w.j == 0 && w.x == 0 && ok) ok = load_q(w.kv);
             }
         }
         // let every copy this warp started land before the CTA can exit
@@ -586,7 +625,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         // ============================ MMA issuer ============================
         const uint32_t IDESC_QK = idesc_bf16_f32(kRows, kKeys, false) | (p.negate_qk ? (1u << 13) : 0u);
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(kRows, D, true);
-        uint32_t fbase = 0;                    // ring position of this unit's K_0
+        uint32_t f = 0;                        // ring position
         uint32_t qcons = 0;                    // Q tiles consumed
         uint32_t puse[2] = {0, 0};             // P_j waits per tile
         int units[2] = {0, 0};                 // units in which the tile had work
@@ -619,37 +658,53 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             if (__shfl_sync(0xffffffffu, u.seq, 0) < 0) break;
             const int nk[2] = {__shfl_sync(0xffffffffu, u.nk[0], 0), __shfl_sync(0xffffffffu, u.nk[1], 0)};
             const int nkv = max(nk[0], nk[1]);
+            // the S after which Q_x is not read again (split: A and B share one Q)
+            auto last_q = [&](int x, int j) {
+                return p.split ? j == nk[0] - 1 && x == (nk[1] == nk[0] ? 1 : 0) : j == nk[x] - 1;
+            };
             // S of key tile 0: tile A as soon as Q_A and K_0 are in, then tile B
-            if (!mbar_wait(bars + L::B_KVFULL + fbase % R::RING, (fbase / R::RING) & 1, abort_flag, p.err)) break;
             uint32_t qsl[2] = {0, 0};
-            for (int x = 0; x < 2 && ok; ++x) {
+            bool have = false;
+            for (int x = 0; x < 2; ++x) {
                 if (nk[x] == 0) continue;
-                qsl[x] = qcons % QBUFS;
-                if (!mbar_wait(bars + L::B_QFULL + qsl[x], (qcons / QBUFS) & 1, abort_flag, p.err)) {
+                if (!have && !mbar_wait(bars + L::B_KVFULL + f % R::RING, (f / R::RING) & 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
-                ++qcons;
+                have = true;
+                if (x == 1 && p.split) {
+                    qsl[1] = qsl[0];
+                } else {
+                    qsl[x] = qcons % QBUFS;
+                    if (!mbar_wait(bars + L::B_QFULL + qsl[x], (qcons / QBUFS) & 1, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    ++qcons;
+                }
                 tc_fence_after();
+                const bool done = p.split || x == 1 || nk[1] == 0;   // with this K tile
                 if (lane == 0) {
-                    issue_qk(x, fbase % R::RING, qsl[x]);
-                    if (nk[x] == 1) umma_commit(bars + L::B_QEMPTY + qsl[x]);
+                    issue_qk(x, f % R::RING, qsl[x]);
+                    if (last_q(x, 0)) umma_commit(bars + L::B_QEMPTY + qsl[x]);
+                    if (done) umma_commit(bars + L::B_KVEMPTY + f % R::RING);
                 }
                 __syncwarp();
-            }
-            if (!ok) break;
-            if (lane == 0) umma_commit(bars + L::B_KVEMPTY + fbase % R::RING);
-            __syncwarp();
-            for (int j = 0; j < nkv && ok; ++j) {
-                const uint32_t fv = fbase + 2 * (uint32_t)j + 1, fk = fv + 1;
-                const int vslot = fv % R::RING, kslot = fk % R::RING;
-                if (!mbar_wait(bars + L::B_KVFULL + vslot, (fv / R::RING) & 1, abort_flag, p.err)) {
-                    ok = false;
-                    break;
+                if (done) {
+                    ++f;
+                    have = false;
                 }
-                bool k_next = false;
+            }
+            for (int j = 0; j < nkv && ok; ++j) {
+                bool v_here = false, k_here = false;
                 for (int x = 0; x < 2; ++x) {
                     if (j >= nk[x]) continue;
+                    const uint32_t fv = f, fk = f + 1;   // V_j and K_{j+1}
+                    if (!v_here && !mbar_wait(bars + L::B_KVFULL + fv % R::RING, (fv / R::RING) & 1, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    v_here = true;
                     if (!mbar_wait(bars + L::B_PFULL + x, puse[x] & 1, abort_flag, p.err)) {
                         ok = false;
                         break;
@@ -663,34 +718,36 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     tc_fence_after();
                     // P V first: it does not need K_{j+1}, which may still be in flight
                     if (lane == 0) {
-                        issue_pv(x, vslot, j > 0);
+                        issue_pv(x, fv % R::RING, j > 0);
                         if (j == nk[x] - 1) umma_commit(bars + L::B_OFINAL + x);
                     }
                     __syncwarp();
                     if (j + 1 < nk[x]) {
-                        if (!k_next) {
-                            if (!mbar_wait(bars + L::B_KVFULL + kslot, (fk / R::RING) & 1, abort_flag, p.err)) {
+                        if (!k_here) {
+                            if (!mbar_wait(bars + L::B_KVFULL + fk % R::RING, (fk / R::RING) & 1, abort_flag, p.err)) {
                                 ok = false;
                                 break;
                             }
-                            k_next = true;
+                            k_here = true;
                             tc_fence_after();
                         }
                         if (lane == 0) {
-                            issue_qk(x, kslot, qsl[x]);
-                            if (j + 2 == nk[x]) umma_commit(bars + L::B_QEMPTY + qsl[x]);
+                            issue_qk(x, fk % R::RING, qsl[x]);
+                            if (last_q(x, j + 1)) umma_commit(bars + L::B_QEMPTY + qsl[x]);
                         }
                         __syncwarp();
                     }
+                    if (p.split || x == 1 || j >= nk[1]) {   // done with these tiles
+                        if (lane == 0) {
+                            umma_commit(bars + L::B_KVEMPTY + fv % R::RING);
+                            if (k_here) umma_commit(bars + L::B_KVEMPTY + fk % R::RING);
+                        }
+                        __syncwarp();
+                        f += k_here ? 2 : 1;
+                        v_here = k_here = false;
+                    }
                 }
-                if (!ok) break;
-                if (lane == 0) {
-                    umma_commit(bars + L::B_KVEMPTY + vslot);
-                    if (k_next) umma_commit(bars + L::B_KVEMPTY + kslot);
-                }
-                __syncwarp();
             }
-            fbase += 2 * (uint32_t)nkv;
             for (int x = 0; x < 2; ++x) {
                 if (nk[x] > 0) ++units[x];
             }
@@ -725,14 +782,14 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         for (int n = 0;; ++n) {
             const ChunkUnit u = claim(n);
             if (u.seq < 0) break;
-            const uint32_t vfill = fbase + 1;   // ring position of V_0
-            fbase += 2 * (uint32_t)u.nkv();
+            const uint32_t unit_base = fbase;
+            fbase += 2 * (uint32_t)(u.sn[0] + u.sn[1]);
             const int nk = x ? u.nk[1] : u.nk[0], ntok = x ? u.ntok[1] : u.ntok[0];   // (no indexed copy)
             if (nk == 0) continue;
             const Keys& keys = u.keys;
             // a warp whose rows are all behind the tile's last one only keeps the protocol
             const bool idle = quarter * 32 >= ntok * p.group;
-            const int pos = keys.p_first + x * p.tq + min(rtok, ntok - 1);
+            const int pos = keys.p_first + x * p.b_step + min(rtok, ntok - 1);
             // virtual keys that the row sees: [0, va) and [vb, vc)
             const int va = p.window > 0 ? min(p.sinks, pos + 1) : 0;
             const int vb = p.window > 0 ? max(0, pos - p.window + 1) - keys.skip : 0;
@@ -741,6 +798,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const int pa = p.window > 0 ? min(p.sinks, keys.p_first + 1) : 0;
             const int pb = p.window > 0 ? max(0, keys.p_first - p.window + 1) - keys.skip : 0;
             const int pc = keys.upto(keys.p_last);
+            const int v0 = u.first_key(p, x);
             const int a_min = __reduce_min_sync(0xffffffffu, va);
             const int b_max = __reduce_max_sync(0xffffffffu, vb);
             const int c_min = __reduce_min_sync(0xffffffffu, vc);
@@ -753,7 +811,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 }
                 ++s_use;
                 tc_fence_after();
-                const int base = u.v0 + j * kKeys;
+                const int base = v0 + j * kKeys;
                 if (!idle) {
                     // no mask anywhere in the warp
                     const bool open = base + kKeys <= c_min && (base >= b_max || base + kKeys <= a_min);
@@ -799,8 +857,12 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     // V rows that nobody in the pair sees hold stale values, or what the ring
                     // held before: zeroed here, a row per thread, by the warps of the first tile
                     // whose P V reads them (the widening does it for the e4m3 cache)
-                    if ((base + kKeys > pc || (base < pb && base + kKeys > pa)) && (x == 0 || j >= u.nk[0])) {
-                        const uint32_t fv = vfill + 2 * (uint32_t)j;
+                    if ((base + kKeys > pc || (base < pb && base + kKeys > pa)) && (p.split || x == 0 || j >= u.nk[0])) {
+                        // ring position of V_j: behind the K_0s and 2 j tiles of this stream, and
+                        // what the other stream has passed
+                        const int sn1 = u.sn[1];
+                        uint32_t fv = unit_base + 1 + 2 * j + (sn1 > 0 ? 1 + min(j, sn1) + min(j, sn1 - 1) : 0);
+                        if (p.split && x == 1) fv += j + 1 < u.sn[0] ? 2 : 1;
                         if (!mbar_wait(bars + L::B_KVFULL + fv % R::RING, (fv / R::RING) & 1, abort_flag, p.err)) {
                             ok = false;
                             break;
@@ -827,10 +889,11 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             // (a sum that is not a number keeps the row from looking empty)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            const size_t orow = (size_t)(u.row0 + x * p.tq + rtok) * p.hq + u.hk * p.group + rhead;
+            const size_t orow = (size_t)(u.row0 + x * p.b_step + rtok) * p.hq + u.hk * p.group + rhead;
             const bool partial = (x ? u.ns[1] : u.ns[0]) > 1;
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
-            float* pdst = p.o_part + (orow * p.s_max + u.part) * D;
+            const size_t prow = orow * p.s_max + u.part + (x && p.split ? 1 : 0);
+            float* pdst = p.o_part + prow * D;
             // (loops stay rolled where they can: the warps of a sub-partition share its instruction
             // cache, and a unit's boundary is code that runs once in many key tiles)
 #pragma unroll 1
@@ -870,7 +933,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 }
             }
             if (row_ok) {
-                if (partial) __stcg(p.lse_part + orow * p.s_max + u.part, lse);
+                if (partial) __stcg(p.lse_part + prow, lse);
                 else if (p.lse_out != nullptr) p.lse_out[orow] = lse;
             }
             pv_before += (uint32_t)nk;
@@ -888,15 +951,16 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 const ChunkUnit u = claim(n);
                 if (u.seq < 0) break;
                 const Keys keys = u.keys;
-                const int nkv = u.nkv();
-                for (int j = 0; j < 2 * nkv && ok; ++j, ++fill) {   // K_0, V_0, K_1, ...
+                const int sn0 = u.sn[0], sn1 = u.sn[1];
+                TileWalk w;
+                for (int i = 0; i < 2 * (sn0 + sn1) && ok; ++i, ++fill, w.next(sn0, sn1)) {
                     const int slot = fill % R::STAGES, ring = fill % R::RING;
                     if (!mbar_wait(bars + L::B_STFULL + slot, (fill / R::STAGES) & 1, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
                     // rows that nobody in the pair sees, or whose block id is bad, become zero
-                    const int key = keys.real(u.v0 + (j >> 1) * kKeys + r);
+                    const int key = keys.real(u.first_key(p, w.x) + w.j * kKeys + r);
                     const bool seen = ((stage_mask[slot * kProducers + prow % kProducers] >> (prow / kProducers)) & 1) && key <= keys.p_last &&
                                       (p.window == 0 || key > keys.p_first - p.window || key < p.sinks);
                     const RowScale f = row_scale(smem[L::SCALE_OFF + slot * kKeys + r]);
@@ -1009,7 +1073,7 @@ cudaError_t launch_chunk(const CUtensorMap& qm, const CUtensorMap& km, const CUt
 }
 
 struct ChunkGeometry {
-    int tq, row_pairs, chunk, s_max;
+    int tq, row_pairs, chunk, split, s_max;
     long long pairs;     // bound on the call's pairs
     size_t nsplit, entries, lse_part, o_part, total;
 };
@@ -1029,12 +1093,34 @@ ChunkGeometry chunk_geometry(int batch, int total_q, int max_q, int hq, int hkv,
     long long keys = std::max(1, max_ctx);
     if (window > 0) keys = std::min(keys, (long long)window + two + (long long)sinks + 2 * kGran);
     const long long tiles = (keys + kKeys - 1) / kKeys;
-    // Partitions only when whole ranges would leave SMs without a unit: each costs a pipeline
-    // fill of about 1.5 key tiles and a float32 partial of every row.
+    g.split = max_q <= g.tq;
     const long long units = std::max(1LL, g.pairs * hkv);
-    long long parts = num_splits > 0 ? num_splits : std::max(1LL, 148LL / units);
-    long long chunk = std::max(1LL, (tiles + parts - 1) / parts);
-    if (num_splits == 0) chunk = std::max(chunk, std::min(tiles, 4LL));
+    long long chunk;
+    if (num_splits > 0) {
+        chunk = std::max(1LL, (tiles + num_splits - 1) / num_splits);
+    } else {
+        // Units per pair: the number n that gives the least time in key tiles of a pair (2.2 us):
+        // rounds of units on 148 SMs, each with about 4 tiles to fill and drain its pipeline;
+        // more than one unit also writes and reads a float32 partial per row and partition
+        // (14 MB per tile) and launches the merge.  (A split unit works on two partitions at
+        // once, so it has partials anyway.  16 windowed chunks of 256 tokens, 256 units: whole
+        // 72 us, two parts each 140; 512-token chunks over 8 k tokens, 512 units: 513 and 616;
+        // 32-row chunks over 8 k tokens, 64 split units of 64 tiles: 127 us as they are, 72 cut
+        // in two.)
+        const int lanes = g.split ? 2 : 1;
+        const long long row_bytes = (long long)total_q * hq * head_dim * 8;
+        long long best = 0, parts = 1;
+        for (long long n = 1; n <= std::min(tiles, 64LL); ++n) {
+            const long long rounds = (units * n + 147) / 148;
+            const long long merge = n > 1 || g.split ? 3 + n * lanes * row_bytes / 14000000 : 0;
+            const long long cost = rounds * ((tiles + n * lanes - 1) / (n * lanes) + 4) + merge;
+            if (n == 1 || cost < best) {
+                best = cost;
+                parts = n;
+            }
+        }
+        chunk = std::max(1LL, (tiles + parts * lanes - 1) / (parts * lanes));
+    }
     // the partition index stays in 15 bits
     chunk = std::max(chunk, (tiles + 32766) / 32767);
     g.chunk = (int)chunk;
@@ -1113,6 +1199,9 @@ nvpa_status_t run_chunk_tiles(const WindowCall& c, cudaStream_t stream) {
     p.block_size = c.block_size;
     p.block_shift = __builtin_ctz((unsigned)c.block_size);
     p.chunk = g.chunk;
+    p.split = g.split;
+    p.b_step = g.split ? 0 : g.tq;
+    p.unit_tiles = g.split ? 2 * g.chunk : g.chunk;
     p.s_max = g.s_max;
     p.max_entries = (int)(g.pairs * g.s_max);
     // the scale multiplies raw scores as a positive factor; a negative one flips the sign of

@@ -1,6 +1,7 @@
 // The extern "C" entry points of libnvpa: argument checks, then the launches.
 // Every check that needs only host-side values happens here, before anything is
 // enqueued; device-side values (slots, block ids, lengths) are checked in the kernels.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -473,13 +474,14 @@ nvpa_status_t nvpa_paged_decode_attention_window(
     return st != NVPA_OK || empty ? st : run_row_attention(c, stream);
 }
 
-// Which kernel a chunk call takes: up to kRowKernelRows query rows per KV head (tokens times
-// heads of its group) go to the row kernel, which reads the keys once for 24 rows; more go to
-// the 128-row tiles.  (8 contexts of 8 k keys in 8 bits, 32 / 8 heads: 20 rows 65 us by rows,
-// 91 by tiles; 32 rows 106 and 92.)
-constexpr int kRowKernelRows = 24;
-static bool chunk_on_tiles(int max_seqlen_q, int num_q_heads, int num_kv_heads) {
-    return (long long)max_seqlen_q * (num_q_heads / num_kv_heads) > kRowKernelRows;
+// Which kernel a chunk call takes: few query rows per KV head (tokens times heads of its group)
+// go to the row kernel, which reads the keys once for 16 rows (24 of an e4m3 cache); more go to
+// the 128-row tiles.  (8 contexts of 8 k keys, 32 / 8 heads, e4m3 cache: 16 rows 49 us by rows
+// and 72 by tiles, 20 rows 65 and 72, 32 rows 106 and 72; bf16 cache: 12 rows 65 and 62, 20 rows
+// 75 and 62.)
+constexpr int kRowKernelRows = 16, kRowKernelRowsE4m3 = 24;
+static bool chunk_on_tiles(int max_seqlen_q, int num_q_heads, int num_kv_heads, bool e4m3) {
+    return (long long)max_seqlen_q * (num_q_heads / num_kv_heads) > (e4m3 ? kRowKernelRowsE4m3 : kRowKernelRows);
 }
 
 size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_heads, int num_kv_heads,
@@ -488,11 +490,16 @@ size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_hea
     if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || !attn_block_size_ok(block_size) ||
         !window_sizes_ok(num_q_heads, num_kv_heads, head_dim, max_context_len, window, num_sinks, num_splits))
         return 0;
-    return chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads)
-               ? chunk_tiles_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
-                                             max_context_len, window, num_sinks, num_splits)
-               : row_attention_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
-                                               max_context_len, window, num_sinks, num_splits);
+    // one size for either type of cache
+    size_t bytes = 0;
+    if (chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads, false))
+        bytes = chunk_tiles_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads, num_kv_heads, head_dim,
+                                            max_context_len, window, num_sinks, num_splits);
+    if (!chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads, true))
+        bytes = std::max(bytes, row_attention_workspace_bytes(batch, total_q, max_seqlen_q, num_q_heads,
+                                                              num_kv_heads, head_dim, max_context_len, window,
+                                                              num_sinks, num_splits));
+    return bytes;
 }
 
 nvpa_status_t nvpa_chunk_attention(
@@ -511,8 +518,8 @@ nvpa_status_t nvpa_chunk_attention(
     const nvpa_status_t st = check_window_call(c, cache_type, &empty);
     if (st != NVPA_OK || empty) return st;
     NVPA_REQUIRE(cu_seqlens_q != nullptr, NVPA_ERR_INVALID_ARG, "null pointer");
-    return chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads) ? run_chunk_tiles(c, stream)
-                                                                   : run_row_attention(c, stream);
+    return chunk_on_tiles(max_seqlen_q, num_q_heads, num_kv_heads, cache_type == NVPA_CACHE_E4M3)
+               ? run_chunk_tiles(c, stream) : run_row_attention(c, stream);
 }
 
 nvpa_status_t nvpa_check_bounded_wait(int32_t* err_flag, cudaStream_t stream) {

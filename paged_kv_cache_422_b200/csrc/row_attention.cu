@@ -936,7 +936,7 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     if (c.head_dim == DD && fp8 == FF && r.nt == NN) e = launch_rows<DD, FF, NN>(p, max_items, stream);
     NVPA_CASE(128, false, 1) NVPA_CASE(128, false, 2) NVPA_CASE(128, true, 1) NVPA_CASE(128, true, 2)
     NVPA_CASE(64, false, 1) NVPA_CASE(64, false, 2) NVPA_CASE(64, true, 1) NVPA_CASE(64, true, 2)
-    NVPA_CASE(128, false, 3) NVPA_CASE(128, true, 3) NVPA_CASE(64, false, 3) NVPA_CASE(64, true, 3)
+    NVPA_CASE(128, true, 3) NVPA_CASE(64, true, 3)   // (bf16: up to 16 rows)
 #undef NVPA_CASE
     if (e != cudaSuccess) return cuda_failure(e, "row attention launch");
     if (r.s_max > 1) {
