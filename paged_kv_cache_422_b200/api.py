@@ -324,42 +324,78 @@ def lse_combine(o_parts, lse_parts, out=None, lse_out=None, stream=None, return_
 # the 8-bit cache, the sliding window and chunks of new tokens
 # ------------------------------------------------------------------------------------
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+# These calls are a few microseconds of GPU work at small sizes, so a well-formed call takes one
+# comparison per tensor; only a refused one goes through the checks that name the fault.
+
+def _expect(t, dtype, name, ndim, index, contiguous=True):
+    """Refuse t unless it is a `dtype` tensor of ndim dimensions (None: any) on CUDA device
+    `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
+            and t.get_device() == index and t.is_contiguous()):
+        return
+    _need(t, dtype, name, ndim)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if contiguous:
+        _contig(t, name)
 
 
-def _on_device(device, stream):
-    """The stream handle for a call on `device`, which is made current for the launch."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return torch.cuda.device(device), int(s.cuda_stream)
+def _raw_stream(index, stream):
+    """The handle of the stream to launch on, the current one of device `index` by default."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)   # (no Stream object: 1 us less)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
 
 
-def _fp8_cache(cache, scales, cache_name="cache", scales_name="scales"):
-    """Dimensions of one e4m3 pool [num_blocks, block_size, Hkv, D] with its scale bytes
-    [num_blocks, Hkv, block_size]."""
-    _need(cache, _FP8, cache_name, 4)
-    _need(scales, _U8, scales_name, 3)
-    _contig(cache, cache_name)
-    _contig(scales, scales_name)
-    nb, bs, hkv, d = (int(x) for x in cache.shape)
-    if tuple(scales.shape) != (nb, hkv, bs):
+def _empty(shape, dtype, index, stream):
+    """Memory for a call on `stream`, from that stream's pool: a workspace that is freed at
+    return, or memory that work queued elsewhere still uses, is then never handed out early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+
+
+def _call(name, index, *args):
+    """Call a C entry point with device `index` current."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    check(st, name)
+
+
+def _fp8_cache(cache, scales, cache_name="cache", scales_name="scales", index=None):
+    """(dimensions, device index) of one e4m3 pool [num_blocks, block_size, Hkv, D] with its
+    scale bytes [num_blocks, Hkv, block_size]."""
+    if index is None:
+        _need(cache, _FP8, cache_name, 4)
+        index = cache.get_device()
+    _expect(cache, _FP8, cache_name, 4, index)
+    _expect(scales, _U8, scales_name, 3, index)
+    nb, bs, hkv, d = cache.shape
+    if scales.shape != (nb, hkv, bs):
         raise ValueError(f"{scales_name} must be [{nb}, {hkv}, {bs}], got {tuple(scales.shape)}")
-    return nb, bs, hkv, d
+    return (nb, bs, hkv, d), index
 
 
 def _any_cache(k_cache, v_cache, k_scales, v_scales):
+    """(num_blocks, block_size, Hkv, D), cache type and device index of a pair of pools."""
     if (k_scales is None) != (v_scales is None):
         raise ValueError("k_scales and v_scales must be given together")
     if k_scales is None:
-        return _cache_dims(k_cache, v_cache) + (NVPA_CACHE_BF16,)
-    dims = _fp8_cache(k_cache, k_scales, "k_cache", "k_scales")
-    if _fp8_cache(v_cache, v_scales, "v_cache", "v_scales") != dims:
+        dims = _cache_dims(k_cache, v_cache)
+        index = k_cache.get_device()
+        _expect(v_cache, _BF16, "v_cache", 4, index)
+        return dims, NVPA_CACHE_BF16, index
+    dims, index = _fp8_cache(k_cache, k_scales, "k_cache", "k_scales")
+    if _fp8_cache(v_cache, v_scales, "v_cache", "v_scales", index)[0] != dims:
         raise ValueError("k_cache and v_cache shapes differ")
-    return dims + (NVPA_CACHE_E4M3,)
+    return dims, NVPA_CACHE_E4M3, index
 
 
 def store_kvcache_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, err_flag=None,
@@ -368,83 +404,86 @@ def store_kvcache_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, 
     caches ([num_blocks, block_size, Hkv, D] float8_e4m3fn) at slot_mapping[t], one scale
     byte per (slot, KV head) in k_scales / v_scales ([num_blocks, Hkv, block_size] uint8:
     a value is code * 2^(byte - 127)); slot -1 skips the token."""
-    nb, bs, hkv, d, _ = _any_cache(k_cache, v_cache, k_scales, v_scales)
+    (nb, bs, hkv, d), _, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
     if k_scales is None:
         raise TypeError("k_scales and v_scales are required")
-    _need(k, _BF16, "k", 3)
-    _need(v, _BF16, "v", 3)
-    _need(slot_mapping, _I32, "slot_mapping", 1)
-    _contig(slot_mapping, "slot_mapping")
-    n = int(slot_mapping.shape[0])
+    _expect(k, _BF16, "k", 3, index, contiguous=False)
+    _expect(v, _BF16, "v", 3, index, contiguous=False)
+    _expect(slot_mapping, _I32, "slot_mapping", 1, index)
+    n = slot_mapping.shape[0]
     for name, t in (("k", k), ("v", v)):
-        if tuple(t.shape) != (n, hkv, d):
+        if t.shape != (n, hkv, d):
             raise ValueError(f"{name} must be [{n}, {hkv}, {d}], got {tuple(t.shape)}")
-        if n and (t.stride(2) != 1 or t.stride(1) != d):
+        if n and not t.is_contiguous() and (t.stride(2) != 1 or t.stride(1) != d):
             raise ValueError(f"{name}: heads and dims of a token must be contiguous")
     if err_flag is not None:
-        _need(err_flag, _I32, "err_flag")
-    _same_device(k_cache.device, k=k, v=v, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                 slot_mapping=slot_mapping, err_flag=err_flag)
-    dev, handle = _on_device(k_cache.device, stream)
-    with dev:
-        st = lib().nvpa_store_kvcache_fp8(
-            _ptr(k), _ptr(v), k.stride(0), v.stride(0), _ptr(k_cache), _ptr(v_cache),
-            _ptr(k_scales), _ptr(v_scales), _ptr(slot_mapping), n, hkv, d, nb, bs, _ptr(err_flag),
-            handle)
-    check(st, "nvpa_store_kvcache_fp8")
+        _expect(err_flag, _I32, "err_flag", None, index)
+    _call(
+        "nvpa_store_kvcache_fp8", index,
+        k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(),
+        n, hkv, d, nb, bs, _ptr(err_flag), _raw_stream(index, stream))
 
 
 def gather_kv_fp8(cache, scales, block_tables, cu_seqlens_k, total_k, out=None, err_flag=None,
                   stream=None):
     """Each sequence's rows of an e4m3 pool read back as bf16: [total_k, Hkv, D]."""
-    nb, bs, hkv, d = _fp8_cache(cache, scales)
-    for name, t, nd in (("block_tables", block_tables, 2), ("cu_seqlens_k", cu_seqlens_k, 1)):
-        _need(t, _I32, name, nd)
-        _contig(t, name)
-    batch = int(cu_seqlens_k.shape[0]) - 1
+    (nb, bs, hkv, d), index = _fp8_cache(cache, scales)
+    _expect(block_tables, _I32, "block_tables", 2, index)
+    _expect(cu_seqlens_k, _I32, "cu_seqlens_k", 1, index)
+    batch = cu_seqlens_k.shape[0] - 1
     if batch < 0 or block_tables.shape[0] != batch:
         raise ValueError("cu_seqlens_k must have one entry more than block_tables has rows")
-    shape = (int(total_k), hkv, d)
+    total_k = int(total_k)
+    shape = (total_k, hkv, d)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=cache.device)
-    _need(out, _BF16, "out", 3)
-    _contig(out, "out")
-    if tuple(out.shape) != shape:
-        raise ValueError(f"out must be {list(shape)}, got {tuple(out.shape)}")
+        out = _empty(shape, _BF16, index, stream)
+    else:
+        _expect(out, _BF16, "out", 3, index)
+        if out.shape != shape:
+            raise ValueError(f"out must be {list(shape)}, got {tuple(out.shape)}")
     if err_flag is not None:
-        _need(err_flag, _I32, "err_flag")
-    _same_device(cache.device, scales=scales, block_tables=block_tables, cu_seqlens_k=cu_seqlens_k,
-                 out=out, err_flag=err_flag)
-    dev, handle = _on_device(cache.device, stream)
-    with dev:
-        st = lib().nvpa_gather_kv_fp8(
-            _ptr(out), _ptr(cache), _ptr(scales), _ptr(block_tables), int(block_tables.shape[1]),
-            _ptr(cu_seqlens_k), batch, int(total_k), hkv, d, nb, bs, _ptr(err_flag), handle)
-    check(st, "nvpa_gather_kv_fp8")
+        _expect(err_flag, _I32, "err_flag", None, index)
+    _call(
+        "nvpa_gather_kv_fp8", index,
+        out.data_ptr(), cache.data_ptr(), scales.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], cu_seqlens_k.data_ptr(), batch, total_k, hkv, d, nb, bs,
+        _ptr(err_flag), _raw_stream(index, stream))
     return out
 
 
-def _window_outputs(q, hkv, d, out, lse, return_lse, rows_name):
+def _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, rows_name):
     """Checks of q and the outputs; (query rows, query heads, out, lse)."""
-    _need(q, _BF16, "q", 3)
-    _contig(q, "q")
-    n, hq, dq = (int(x) for x in q.shape)
+    _expect(q, _BF16, "q", 3, index)
+    n, hq, dq = q.shape
     if dq != d:
         raise ValueError("q head_dim differs from the cache's")
     if out is None:
-        out = torch.empty_like(q)
-    _need(out, _BF16, "out", 3)
-    _contig(out, "out")
-    if out.shape != q.shape:
-        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    if return_lse and lse is None:
-        lse = torch.empty((n, hq), dtype=torch.float32, device=q.device)
+        out = _empty(q.shape, _BF16, index, stream)
+    else:
+        _expect(out, _BF16, "out", 3, index)
+        if out.shape != q.shape:
+            raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
     if lse is not None:
-        _need(lse, torch.float32, "lse", 2)
-        _contig(lse, "lse")
-        if tuple(lse.shape) != (n, hq):
+        _expect(lse, torch.float32, "lse", 2, index)
+        if lse.shape != (n, hq):
             raise ValueError(f"lse must be [{rows_name}, Hq] = [{n}, {hq}], got {tuple(lse.shape)}")
+    elif return_lse:
+        lse = _empty((n, hq), torch.float32, index, stream)
     return n, hq, out, lse
+
+
+def _workspace(workspace, index, stream, size, *args):
+    """A workspace of size(*args) bytes, or the caller's; (pointer, bytes, tensor)."""
+    if workspace is None:
+        workspace = _empty(size(*args), _U8, index, stream)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    elif workspace.get_device() != index:
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{index}")
+    else:
+        _contig(workspace, "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def paged_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_context_len,
@@ -461,32 +500,26 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
     """Decode attention over a bf16 cache, or an e4m3 one with its k_scales / v_scales: q
     [B, Hq, D] bf16, one query per sequence, which sees the last `window` keys (0: all) and
     the first `num_sinks`."""
-    nb, bs, hkv, d, kind = _any_cache(k_cache, v_cache, k_scales, v_scales)
-    b, hq, out, lse = _window_outputs(q, hkv, d, out, lse, return_lse, "B")
-    for name, t, nd in (("block_tables", block_tables, 2), ("context_lens", context_lens, 1)):
-        _need(t, _I32, name, nd)
-        _contig(t, name)
-        if t.shape[0] != b:
-            raise ValueError(f"{name}: batch differs from q's")
+    (nb, bs, hkv, d), kind, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
+    b, hq, out, lse = _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, "B")
+    _expect(block_tables, _I32, "block_tables", 2, index)
+    _expect(context_lens, _I32, "context_lens", 1, index)
+    if block_tables.shape[0] != b:
+        raise ValueError("block_tables: batch differs from q's")
+    if context_lens.shape[0] != b:
+        raise ValueError("context_lens: batch differs from q's")
     if err_flag is not None:
-        _need(err_flag, _I32, "err_flag")
-    if workspace is None:
-        workspace = torch.empty(paged_decode_window_workspace_size(
-            b, hq, hkv, d, max_context_len, bs, window, num_sinks, num_splits), dtype=_U8,
-            device=q.device)
-    _contig(workspace, "workspace")
-    _same_device(k_cache.device, q=q, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                 block_tables=block_tables, context_lens=context_lens, out=out, lse=lse,
-                 workspace=workspace, err_flag=err_flag)
-    dev, handle = _on_device(k_cache.device, stream)
-    with dev:
-        st = lib().nvpa_paged_decode_attention_window(
-            _ptr(out), _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), kind, _ptr(k_scales),
-            _ptr(v_scales), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), b,
-            hq, hkv, d, nb, bs, int(max_context_len), float(softmax_scale), int(window),
-            int(num_sinks), int(num_splits), _ptr(workspace),
-            int(workspace.numel() * workspace.element_size()), _ptr(err_flag), handle)
-    check(st, "nvpa_paged_decode_attention_window")
+        _expect(err_flag, _I32, "err_flag", None, index)
+    ws, ws_bytes, workspace = _workspace(
+        workspace, index, stream, paged_decode_window_workspace_size, b, hq, hkv, d, max_context_len, bs,
+        window, num_sinks, num_splits)
+    _call(
+        "nvpa_paged_decode_attention_window", index,
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind,
+        _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), b, hq, hkv, d, nb, bs, int(max_context_len),
+        float(softmax_scale), int(window), int(num_sinks), int(num_splits), ws, ws_bytes,
+        _ptr(err_flag), _raw_stream(index, stream))
     return (out, lse) if return_lse else out
 
 
@@ -506,33 +539,24 @@ def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_len
     cu_seqlens_q[i+1]-1, [total_q, Hq, D] bf16) over its context_lens[i] cached keys, the new
     ones included, in a bf16 cache, or an e4m3 one with its k_scales / v_scales; a query sees
     the last `window` keys up to its own (0: all) and the first `num_sinks`."""
-    nb, bs, hkv, d, kind = _any_cache(k_cache, v_cache, k_scales, v_scales)
-    total_q, hq, out, lse = _window_outputs(q, hkv, d, out, lse, return_lse, "total_q")
-    for name, t, nd in (("block_tables", block_tables, 2), ("cu_seqlens_q", cu_seqlens_q, 1),
-                        ("context_lens", context_lens, 1)):
-        _need(t, _I32, name, nd)
-        _contig(t, name)
-    batch = int(context_lens.shape[0])
+    (nb, bs, hkv, d), kind, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
+    total_q, hq, out, lse = _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, "total_q")
+    _expect(block_tables, _I32, "block_tables", 2, index)
+    _expect(cu_seqlens_q, _I32, "cu_seqlens_q", 1, index)
+    _expect(context_lens, _I32, "context_lens", 1, index)
+    batch = context_lens.shape[0]
     if block_tables.shape[0] != batch or cu_seqlens_q.shape[0] != batch + 1:
         raise ValueError("block_tables, cu_seqlens_q and context_lens disagree about the batch")
     if err_flag is not None:
-        _need(err_flag, _I32, "err_flag")
-    if workspace is None:
-        workspace = torch.empty(chunk_attention_workspace_size(
-            batch, total_q, hq, hkv, d, max_seqlen_q, max_context_len, bs, window, num_sinks,
-            num_splits), dtype=_U8, device=q.device)
-    _contig(workspace, "workspace")
-    _same_device(k_cache.device, q=q, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                 block_tables=block_tables, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens,
-                 out=out, lse=lse, workspace=workspace, err_flag=err_flag)
-    dev, handle = _on_device(k_cache.device, stream)
-    with dev:
-        st = lib().nvpa_chunk_attention(
-            _ptr(out), _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), kind, _ptr(k_scales),
-            _ptr(v_scales), _ptr(block_tables), int(block_tables.shape[1]), _ptr(cu_seqlens_q),
-            _ptr(context_lens), batch, total_q, int(max_seqlen_q), int(max_context_len), hq, hkv, d,
-            nb, bs, float(softmax_scale), int(window), int(num_sinks), int(num_splits),
-            _ptr(workspace), int(workspace.numel() * workspace.element_size()), _ptr(err_flag),
-            handle)
-    check(st, "nvpa_chunk_attention")
+        _expect(err_flag, _I32, "err_flag", None, index)
+    ws, ws_bytes, workspace = _workspace(
+        workspace, index, stream, chunk_attention_workspace_size, batch, total_q, hq, hkv, d, max_seqlen_q,
+        max_context_len, bs, window, num_sinks, num_splits)
+    _call(
+        "nvpa_chunk_attention", index,
+        out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind,
+        _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
+        cu_seqlens_q.data_ptr(), context_lens.data_ptr(), batch, total_q, int(max_seqlen_q),
+        int(max_context_len), hq, hkv, d, nb, bs, float(softmax_scale), int(window),
+        int(num_sinks), int(num_splits), ws, ws_bytes, _ptr(err_flag), _raw_stream(index, stream))
     return (out, lse) if return_lse else out
