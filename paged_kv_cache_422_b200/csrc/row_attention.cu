@@ -70,6 +70,7 @@ struct RowParams {
     int max_blocks, num_blocks, block_size, block_shift;
     int max_ctx;
     int window, sinks;           // window 0: none
+    int planned;                 // items come from the plan kernel (always for chunks)
     int tok;                     // query tokens per row tile
     int row_tiles;               // row tiles of the longest chunk
     int chunk;                   // 16-key tiles per partition
@@ -104,8 +105,42 @@ __device__ __forceinline__ uint32_t seen_keys(int key0, int p, int window, int s
     return m;
 }
 
+// Row tile i of the call: (sequence, tile of its query tokens); ntok = 0 when there is none.
+struct RowTile {
+    int b, q0, ntok, p0;
+    int tiles, ns;       // 16-key tiles that it sees, partitions
+};
+__device__ __forceinline__ RowTile row_tile(const RowParams& p, int i, bool flag) {
+    const int lim = (int)min((long long)p.max_ctx, (long long)p.max_blocks * p.block_size);
+    RowTile t;
+    t.b = i / p.row_tiles;
+    const int rt = i - t.b * p.row_tiles;
+    int ctx = __ldg(p.context_lens + t.b), lq = 1;
+    t.q0 = t.b;
+    bool ok = ctx >= 0 && ctx <= lim;
+    if (p.cu_q != nullptr) {
+        t.q0 = __ldg(p.cu_q + t.b);
+        const int q1 = __ldg(p.cu_q + t.b + 1);
+        ok = ok && t.q0 >= 0 && q1 >= t.q0 && q1 <= p.total_q && q1 - t.q0 <= p.max_q && q1 - t.q0 <= ctx;
+        lq = ok ? q1 - t.q0 : 0;   // a bad sequence's rows are left unwritten
+    } else {
+        ctx = min(max(ctx, 0), lim);
+    }
+    if (!ok && flag && rt == 0) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
+    t.ntok = min(p.tok, lq - rt * p.tok);
+    t.q0 += rt * p.tok;
+    t.p0 = ctx - lq + rt * p.tok;
+    t.tiles = t.ntok > 0 && t.p0 >= 0 ? tile_range(t.p0, t.p0 + t.ntok - 1, p.window, p.sinks).count : 0;
+    t.ns = t.ntok > 0 ? max(1, (t.tiles + p.chunk - 1) / p.chunk) : 0;
+    return t;
+}
+// Its partitions of the full size; the last one is shorter when there is one more.
+__device__ __forceinline__ int full_parts(const RowParams& p, const RowTile& t) {
+    return t.ns - (t.tiles < t.ns * p.chunk ? 1 : 0);
+}
+
 // ------------------------------------------------------------------------------------
-// plan: context lengths -> items, full partitions first, then the shorter ones, longest
+// plan of chunk calls: context lengths -> items, full partitions first, then the shorter ones, longest
 // first (as the decode plan orders them)
 // ------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
@@ -117,39 +152,10 @@ __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
     if (p.cu_q != nullptr)
         for (int i = tid; i < p.total_q; i += blockDim.x) p.nsplit[i] = 0;
     __syncthreads();
-    const int lim = (int)min((long long)p.max_ctx, (long long)p.max_blocks * p.block_size);
-    struct Tile {
-        int b, q0, ntok, p0, tiles, ns;
-    };
-    // row tile i: (sequence, tile of its query tokens); ntok = 0 when there is none
-    auto tile = [&](int i, bool flag) {
-        Tile t;
-        t.b = i / p.row_tiles;
-        const int rt = i - t.b * p.row_tiles;
-        int ctx = __ldg(p.context_lens + t.b), lq = 1;
-        t.q0 = t.b;
-        bool ok = ctx >= 0 && ctx <= lim;
-        if (p.cu_q != nullptr) {
-            t.q0 = __ldg(p.cu_q + t.b);
-            const int q1 = __ldg(p.cu_q + t.b + 1);
-            lq = q1 - t.q0;
-            ok = ok && t.q0 >= 0 && q1 <= p.total_q && lq >= 0 && lq <= p.max_q && lq <= ctx;
-            if (!ok) lq = 0;   // the sequence's rows are left unwritten
-        } else {
-            ctx = min(max(ctx, 0), lim);
-        }
-        if (!ok && flag && rt == 0) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
-        t.ntok = min(p.tok, lq - rt * p.tok);
-        t.q0 += rt * p.tok;
-        t.p0 = ctx - lq + rt * p.tok;
-        t.tiles = t.ntok > 0 && t.p0 >= 0
-            ? tile_range(t.p0, t.p0 + t.ntok - 1, p.window, p.sinks).count : 0;
-        t.ns = t.ntok > 0 ? max(1, (t.tiles + p.chunk - 1) / p.chunk) : 0;
-        return t;
-    };
+    auto tile = [&](int i, bool flag) { return row_tile(p, i, flag); };
     // (cumulative lengths that run backwards can claim rows twice, and so more entries than
     // the table has room for: what does not fit is dropped and flagged)
-    auto put = [&](int at, const Tile& t, int s) {
+    auto put = [&](int at, const RowTile& t, int s) {
         if (at >= p.max_entries) return;
         p.items[2 * at] = make_int4(t.b, s | (t.ns << 16), t.q0, t.ntok);
         p.items[2 * at + 1] = make_int4(t.p0, s * p.chunk, min(t.tiles, (s + 1) * p.chunk), 0);
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
     const int n = p.batch * p.row_tiles;
     for (int base = 0; base < n; base += blockDim.x) {
         const int i = base + tid;
-        Tile t{};
+        RowTile t{};
         int nfull = 0;
         if (i < n) {
             t = tile(i, true);
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
     if (tid < kLengthClasses) s_cls[cls] = carry + e;
     __syncthreads();
     for (int i = tid; i < n; i += blockDim.x) {
-        const Tile t = tile(i, false);
+        const RowTile t = tile(i, false);
         if (t.ns == 0) continue;
         const int last = t.tiles - (t.ns - 1) * p.chunk;
         if (last == p.chunk) continue;
@@ -274,11 +280,44 @@ row_attention_kernel(const RowParams p) {
     TileRange it_r{};
     const int32_t* it_bt = nullptr;
 
-    pdl_wait();
-    const int total_items = __ldcg(p.counter + 1);
     const int nwarps = gridDim.x * kRowWarps;
     int nx_item = blockIdx.x * kRowWarps + warp;
-
+    // A decode call whose items fit one round has no plan kernel, which would cost 5 us of its
+    // 20 to 100: every CTA counts the sequences' partitions itself, a sequence per thread.  Items
+    // are the full partitions of all sequences, then the shorter last ones, each for every KV
+    // head.  (With several rounds the plan's order and dynamic claims are worth more than its
+    // time: 64 contexts of 0.5 to 4 k keys 72 us with it, 78 without.)
+    __shared__ int s_full[kRowWarps * 32], s_rest[kRowWarps * 32], s_scan[32];
+    int total_items = 0, total_full = 0;
+    if (p.planned) {
+        pdl_wait();
+        total_items = __ldcg(p.counter + 1);
+    } else {
+        int full = 0, rest = 0, total_rest = 0;
+        if ((int)threadIdx.x < p.batch) {
+            const RowTile r = row_tile(p, threadIdx.x, blockIdx.x == 0);
+            full = full_parts(p, r);
+            rest = r.ns - full;
+        }
+        s_full[threadIdx.x] = block_exclusive_scan(full, s_scan, total_full);
+        s_rest[threadIdx.x] = block_exclusive_scan(rest, s_scan, total_rest);
+        __syncthreads();
+        total_items = (total_full + total_rest) * p.hkv;
+    }
+    // item c (of one KV head) without a plan: its sequence is the last one with at most c
+    // partitions before it
+    auto find = [&](int c) {
+        const bool rest = c >= total_full;
+        const int k = rest ? c - total_full : c;
+        const int* before = rest ? s_rest : s_full;
+        int i = -1;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) i += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= k));
+        const RowTile r = row_tile(p, i, false);
+        const int s = rest ? r.ns - 1 : k - before[i];
+        it_a = make_int4(i, s | (r.ns << 16), i, 1);
+        it_b = make_int4(r.p0, s * p.chunk, min(r.tiles, (s + 1) * p.chunk), 0);
+    };
     auto real_tile = [&](int v) { return v < it_r.head ? v : v + it_r.skip; };
     auto load_block = [&]() {   // the table entries of the stage to be issued next (checked there)
 #pragma unroll
@@ -291,12 +330,17 @@ row_attention_kernel(const RowParams p) {
             it_valid = false;
             return;
         }
-        if (lane == 0) nx_item = nwarps + atomicAdd(p.counter, 1);
         it_valid = true;
         const int e = idx / p.hkv;
         it_hk = idx - e * p.hkv;
-        it_a = __ldcg(reinterpret_cast<const int4*>(p.items) + 2 * e);
-        it_b = __ldcg(reinterpret_cast<const int4*>(p.items) + 2 * e + 1);
+        if (p.planned) {
+            if (lane == 0) nx_item = nwarps + atomicAdd(p.counter, 1);
+            it_a = __ldcg(reinterpret_cast<const int4*>(p.items) + 2 * e);
+            it_b = __ldcg(reinterpret_cast<const int4*>(p.items) + 2 * e + 1);
+        } else {
+            nx_item += nwarps;
+            find(e);
+        }
         it_bt = p.block_tables + (size_t)it_a.x * p.max_blocks;
         it_plast = it_b.x + it_a.w - 1;
         it_r = tile_range(max(it_b.x, 0), max(it_plast, 0), p.window, p.sinks);
@@ -469,6 +513,7 @@ row_attention_kernel(const RowParams p) {
 
     auto epilogue = [&]() {
         const int s = a.y & 0xffff, ns = a.y >> 16;
+        if (!p.planned && s == 0 && hk == 0 && lane == 0) p.nsplit[a.x] = ns;   // for the combine
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -806,7 +851,7 @@ cudaError_t launch_rows(const RowParams& p, long long max_items, cudaStream_t st
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.planned ? 1 : 0;   // behind its plan kernel
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -830,9 +875,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 //    lengths that the host does not know (8 contexts of 32 k keys: 24 partitions each 107 us,
 //    27 109, 30, where a second round begins, 146, 64 124).
 // Four tiles at least: shorter items cost more than the warps they fill.
+constexpr long long row_resident_warps(int nt) { return 148LL * kRowWarps * (nt == 1 ? 3 : 2); }   // on a B200
 int row_chunk_tiles(long long pairs, long long seen, int nt, int num_splits) {
     if (num_splits > 0) return (int)std::max(1LL, (seen + num_splits - 1) / num_splits);
-    const long long warps = 148LL * kRowWarps * (nt == 1 ? 3 : 2);   // resident on a B200
+    const long long warps = row_resident_warps(nt);
     long long chunk = 22;
     if (pairs * 8 <= warps) {
         const long long parts = std::max(1LL, warps * 9 / 10 / std::max(1LL, pairs));
@@ -920,15 +966,20 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     p.window = c.window >= c.max_context_len ? 0 : c.window;
     p.sinks = std::min(c.num_sinks, c.max_context_len);
     p.max_entries = (int)(r.tiles * r.s_max);
+    p.planned = c.cu_seqlens_q != nullptr || c.batch > kRowWarps * 32 ||
+                r.tiles * r.s_max * c.hkv > row_resident_warps(r.nt);
     p.tok = r.tok;
     p.row_tiles = r.row_tiles;
     p.chunk = r.chunk;
     p.s_max = r.s_max;
     p.scale_log2 = c.scale * kLog2e;
-    row_plan_kernel<<<1, 1024, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_failure(e, "row attention plan launch");
-    count_launches(1);
+    cudaError_t e = cudaSuccess;
+    if (p.planned) {
+        row_plan_kernel<<<1, 1024, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_failure(e, "row attention plan launch");
+        count_launches(1);
+    }
     const long long max_items = r.tiles * r.s_max * c.hkv;
     const bool fp8 = c.k_scales != nullptr;
     e = cudaErrorInvalidValue;
