@@ -5,6 +5,8 @@
 // Both are bound by HBM bandwidth (3 bytes per value: 2 of bf16, 1 of e4m3), so each value
 // is loaded once with 16-byte loads and the row's maximum never leaves the registers: D / 16
 // lanes hold one row (16 values each), log2(D / 16) shuffles give its largest magnitude.
+// Measured with 8 heads of 128: 24594 tokens stored in 25.4 us (6.0 TB/s, 0.91 of the copy
+// bandwidth), 33 k rows read back in 21.3 us (5.0 TB/s; 204 k rows 5.7 TB/s).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -64,92 +66,137 @@ struct StoreFp8Params {
 };
 
 // LPR = D / 16 lanes per (token, KV head) row pair; consecutive lane groups take
-// consecutive heads, so that a warp reads and writes contiguous memory.
+// consecutive heads, so that a warp reads and writes contiguous memory.  One row pair per lane
+// group and no loop: the rows are read while the slot is (padding tokens' rows too), and the
+// block scheduler evens out the waves.
 template <int D>
 __global__ void __launch_bounds__(256) store_fp8_kernel(const StoreFp8Params p) {
     constexpr int LPR = D / 16;
     const int sub = threadIdx.x % LPR;
-    const long long rows = (long long)p.num_tokens * p.hkv;
-    const long long step = (long long)gridDim.x * (256 / LPR);
-    // the loop bound is that of the warp's first row: every lane takes part in the shuffles
-    const long long first = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-    const long long warp_first = first - (threadIdx.x % 32) / LPR;
-    for (long long d = 0; warp_first + d < rows; d += step) {
-        const long long row = first + d;
-        int slot = -1, h = 0;
-        long long t = 0;
-        if (row < rows) {
-            t = row / p.hkv;
-            h = (int)(row - t * p.hkv);
-            slot = __ldg(p.slots + t);
-            if (slot != -1 && (slot < 0 || (long long)slot >= p.capacity)) {
-                if (sub == 0 && h == 0) flag_error(p.err, NVPA_FLAG_BAD_SLOT);
-                slot = -1;
-            }
-        }
-        uint32_t kw[8] = {}, vw[8] = {};
-        if (slot >= 0) {
-            const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (long long)h * D + sub * 16);
-            const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (long long)h * D + sub * 16);
-            const uint4 a = __ldcs(ks), b = __ldcs(ks + 1), c = __ldcs(vs), e = __ldcs(vs + 1);
-            kw[0] = a.x; kw[1] = a.y; kw[2] = a.z; kw[3] = a.w; kw[4] = b.x; kw[5] = b.y; kw[6] = b.z; kw[7] = b.w;
-            vw[0] = c.x; vw[1] = c.y; vw[2] = c.z; vw[3] = c.w; vw[4] = e.x; vw[5] = e.y; vw[6] = e.z; vw[7] = e.w;
-        }
-        bool kodd, vodd;
-        // both maxima in one word: K's in the high half
-        uint32_t km = lane_amax(kw, kodd), vm = lane_amax(vw, vodd);
-        uint32_t m = km << 16 | vm;
+    const long long row = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    // (every lane takes part in the shuffles)
+    const bool have = row < (long long)p.num_tokens * p.hkv;
+    const int t = have ? (int)(row / p.hkv) : 0;
+    const int h = have ? (int)(row - (long long)t * p.hkv) : 0;
+    int slot = have ? __ldg(p.slots + t) : -1;
+    uint32_t kw[8] = {}, vw[8] = {};
+    if (have) {
+        const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (long long)h * D + sub * 16);
+        const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (long long)h * D + sub * 16);
+        const uint4 a = __ldcs(ks), b = __ldcs(ks + 1), c = __ldcs(vs), e = __ldcs(vs + 1);
+        kw[0] = a.x; kw[1] = a.y; kw[2] = a.z; kw[3] = a.w; kw[4] = b.x; kw[5] = b.y; kw[6] = b.z; kw[7] = b.w;
+        vw[0] = c.x; vw[1] = c.y; vw[2] = c.z; vw[3] = c.w; vw[4] = e.x; vw[5] = e.y; vw[6] = e.z; vw[7] = e.w;
+    }
+    if (slot != -1 && (slot < 0 || (long long)slot >= p.capacity)) {
+        if (sub == 0 && h == 0) flag_error(p.err, NVPA_FLAG_BAD_SLOT);
+        slot = -1;
+    }
+    bool kodd, vodd;
+    // both maxima in one word: K's in the high half
+    uint32_t km = lane_amax(kw, kodd), vm = lane_amax(vw, vodd);
+    uint32_t m = km << 16 | vm;
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (slot < 0) continue;
-        const int kb = scale_byte(m >> 16), vb = scale_byte(m & 0xffffu);
-        const size_t at = ((size_t)slot * p.hkv + h) * D + sub * 16;
-        *reinterpret_cast<uint4*>(p.k_cache + at) = lane_codes(kw, scale_value(254 - kb), kodd);
-        *reinterpret_cast<uint4*>(p.v_cache + at) = lane_codes(vw, scale_value(254 - vb), vodd);
-        if (sub == 0) {
-            const int blk = slot / p.block_size;
-            const size_t sat = ((size_t)blk * p.hkv + h) * p.block_size + (slot - blk * p.block_size);
-            p.k_scales[sat] = (uint8_t)kb;
-            p.v_scales[sat] = (uint8_t)vb;
-        }
+    for (int o = LPR / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (slot < 0) return;
+    const int kb = scale_byte(m >> 16), vb = scale_byte(m & 0xffffu);
+    const size_t at = ((size_t)slot * p.hkv + h) * D + sub * 16;
+    *reinterpret_cast<uint4*>(p.k_cache + at) = lane_codes(kw, scale_value(254 - kb), kodd);
+    *reinterpret_cast<uint4*>(p.v_cache + at) = lane_codes(vw, scale_value(254 - vb), vodd);
+    if (sub == 0) {
+        const int blk = slot / p.block_size;
+        const size_t sat = ((size_t)blk * p.hkv + h) * p.block_size + (slot - blk * p.block_size);
+        p.k_scales[sat] = (uint8_t)kb;
+        p.v_scales[sat] = (uint8_t)vb;
     }
 }
 
-// One warp per destination row; 16 codes (32 bytes of bf16) per lane and step.
+// A block takes tiles of whole rows, about kGatherChunks chunks of 8 codes (16 bytes of bf16
+// each, so that a warp's stores fill whole lines).  Reading a chunk hangs on three loads
+// (sequence, block id, codes), so the slots of the next tile's rows are looked up, a row per
+// thread, while this tile's codes are on their way.
+constexpr int kGatherThreads = 256, kGatherPer = 4, kGatherChunks = kGatherThreads * kGatherPer;
+// Blocks per SM: as many as fit (33 k rows of 8 heads of 128: 4 per SM 24.4 us, 6 23.5, 8 21.3,
+// unlimited 22.6).
+constexpr int kGatherBlocks = 8;
+
+struct GatherFp8Params {
+    uint16_t* dst;
+    const uint8_t* cache;
+    const uint8_t* scales;
+    const int32_t* block_tables;
+    const int32_t* cu;
+    int max_blocks, batch, total_k, hkv, num_blocks, block_size, block_shift;
+    int per_row;           // chunks of a row, hkv * D / 8
+    int tile_rows;
+    uint32_t row_magic;    // ceil(2^32 / per_row): j / per_row = umulhi(j, row_magic) for j * per_row < 2^32
+    int32_t* err;
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) gather_fp8_kernel(
-    uint16_t* __restrict__ dst, const uint8_t* __restrict__ cache, const uint8_t* __restrict__ scales,
-    const int32_t* __restrict__ block_tables, int max_blocks, const int32_t* __restrict__ cu, int batch,
-    int total_k, int hkv, int num_blocks, int block_size, int block_shift, int32_t* err) {
-    constexpr int CPH = D / 16;   // chunks per head
-    const int lane = threadIdx.x & 31;
-    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < total_k;
-         row += (long long)gridDim.x * 8) {
-        int lo = 0, hi = batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (__ldg(cu + mid) <= row) lo = mid; else hi = mid - 1;
+__global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const GatherFp8Params p) {
+    constexpr int CPH = D / 8;                                // chunks per head
+    constexpr int kMaxRows = kGatherChunks / CPH;             // rows of a tile
+    constexpr int kNoRow = -2, kZeroRow = -1;
+    __shared__ int s_slot[2][kMaxRows];
+    auto look_up = [&](int row0, int* slots) {
+        for (int i = threadIdx.x; i < min(p.tile_rows, p.total_k - row0); i += kGatherThreads) {
+            const int row = row0 + i;
+            int lo = 0, hi = p.batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldg(p.cu + mid) <= row) lo = mid; else hi = mid - 1;
+            }
+            const int k0 = __ldg(p.cu + lo), k1 = __ldg(p.cu + lo + 1);
+            const int pos = row - k0;
+            int slot = kNoRow;
+            if (row < k0 || row >= k1 || (long long)pos >= (long long)p.max_blocks * p.block_size) {
+                flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
+            } else {
+                const int blk = checked_block(p.block_tables + (size_t)lo * p.max_blocks, pos, p.block_shift,
+                                              p.num_blocks, p.err);
+                slot = blk < 0 ? kZeroRow : blk * p.block_size + (pos & (p.block_size - 1));
+            }
+            slots[i] = slot;
         }
-        const int k0 = __ldg(cu + lo), k1 = __ldg(cu + lo + 1);
-        const int pos = (int)(row - k0);
-        uint16_t* d = dst + (size_t)row * hkv * D;
-        if (row < k0 || row >= k1 || (long long)pos >= (long long)max_blocks * block_size) {
-            if (lane == 0) flag_error(err, NVPA_FLAG_BAD_LENGTH);
-            continue;
-        }
-        const int blk = checked_block(block_tables + (size_t)lo * max_blocks, pos, block_shift, num_blocks,
-                                      lane == 0 ? err : nullptr);
-        const int r = pos & (block_size - 1);
-        const uint8_t* s = cache + ((size_t)max(blk, 0) * block_size + r) * hkv * D;
-        const uint8_t* sc = scales + (size_t)max(blk, 0) * hkv * block_size + r;
-        for (int c = lane; c < hkv * CPH; c += 32) {
-            uint32_t w[8] = {};
-            if (blk >= 0) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(s) + c);
-                const float f = scale_value(__ldg(sc + (size_t)(c / CPH) * block_size));
-                const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+    };
+    const int step = gridDim.x * p.tile_rows;
+    int row0 = blockIdx.x * p.tile_rows;
+    look_up(row0, s_slot[0]);
+    for (int buf = 0; row0 < p.total_k; buf ^= 1) {
+        __syncthreads();
+        const int n = min(p.tile_rows, p.total_k - row0) * p.per_row;
+        uint4* dst = reinterpret_cast<uint4*>(p.dst) + (size_t)row0 * p.per_row;
+        // (one round, but for rows of more than kGatherChunks chunks)
+        for (int base = 0; base < n; base += kGatherChunks) {
+            uint2 code[kGatherPer];
+            uint32_t scale[kGatherPer];
+            int slot[kGatherPer];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+            for (int k = 0; k < kGatherPer; ++k) {
+                const int j = base + k * kGatherThreads + threadIdx.x;
+                slot[k] = kNoRow;
+                code[k] = make_uint2(0, 0);
+                scale[k] = 127;
+                if (j < n) {
+                    const int r = (int)__umulhi((uint32_t)j, p.row_magic), c = j - r * p.per_row;
+                    slot[k] = s_slot[buf][r];
+                    if (slot[k] >= 0) {
+                        const int blk = slot[k] >> p.block_shift;
+                        code[k] = __ldcs(reinterpret_cast<const uint2*>(p.cache + (size_t)slot[k] * p.hkv * D) + c);
+                        scale[k] = __ldg(p.scales + ((size_t)blk * p.hkv + c / CPH) * p.block_size +
+                                         (slot[k] & (p.block_size - 1)));
+                    }
+                }
+            }
+            if (base == 0 && row0 < p.total_k - step) look_up(row0 + step, s_slot[buf ^ 1]);
+#pragma unroll
+            for (int k = 0; k < kGatherPer; ++k) {
+                if (slot[k] == kNoRow) continue;
+                const float f = scale_value(scale[k]);
+                const uint32_t in[2] = {code[k].x, code[k].y};
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
                     uint32_t a, b;
                     e4m3x4_to_half2(in[i], a, b);
                     const float2 x = __half22float2(*reinterpret_cast<__half2*>(&a));
@@ -157,11 +204,11 @@ __global__ void __launch_bounds__(256) gather_fp8_kernel(
                     w[2 * i] = pack_bf16x2(x.x * f, x.y * f);
                     w[2 * i + 1] = pack_bf16x2(y.x * f, y.y * f);
                 }
+                dst[base + k * kGatherThreads + threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            uint4* o = reinterpret_cast<uint4*>(d) + 2 * c;
-            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
+        if (row0 >= p.total_k - step) break;   // (row0 + step may pass 2^31)
+        row0 += step;
     }
 }
 
@@ -189,7 +236,11 @@ nvpa_status_t run_store_kvcache_fp8(const void* k, const void* v, int64_t k_stri
     p.err = err_flag;
     const long long per = 256 / (head_dim / 16);
     const long long need = ((long long)num_tokens * hkv + per - 1) / per;
-    const int grid = (int)std::max(1LL, std::min<long long>(need, (long long)device_sm_count() * 8));
+    if (need > 0x7fffffffLL) {
+        set_error("more than 2^31-1 thread blocks");
+        return NVPA_ERR_UNSUPPORTED;
+    }
+    const int grid = (int)need;
     if (head_dim == 128) store_fp8_kernel<128><<<grid, 256, 0, stream>>>(p);
     else store_fp8_kernel<64><<<grid, 256, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
@@ -203,16 +254,27 @@ nvpa_status_t run_gather_kv_fp8(void* dst, const void* cache, const uint8_t* sca
                                 const int32_t* cu_seqlens_k, int batch, int total_k, int hkv, int head_dim,
                                 int num_blocks, int block_size, int32_t* err_flag, cudaStream_t stream) {
     if (total_k == 0 || batch == 0) return NVPA_OK;
-    const int grid = (int)std::min<long long>(((long long)total_k + 7) / 8, (long long)device_sm_count() * 16);
-    const int shift = __builtin_ctz((unsigned)block_size);
-    auto* d = static_cast<uint16_t*>(dst);
-    auto* c = static_cast<const uint8_t*>(cache);
-    if (head_dim == 128)
-        gather_fp8_kernel<128><<<grid, 256, 0, stream>>>(d, c, scales, block_tables, max_blocks_per_seq, cu_seqlens_k,
-                                                         batch, total_k, hkv, num_blocks, block_size, shift, err_flag);
-    else
-        gather_fp8_kernel<64><<<grid, 256, 0, stream>>>(d, c, scales, block_tables, max_blocks_per_seq, cu_seqlens_k,
-                                                        batch, total_k, hkv, num_blocks, block_size, shift, err_flag);
+    GatherFp8Params p{};
+    p.dst = static_cast<uint16_t*>(dst);
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.scales = scales;
+    p.block_tables = block_tables;
+    p.cu = cu_seqlens_k;
+    p.max_blocks = max_blocks_per_seq;
+    p.batch = batch;
+    p.total_k = total_k;
+    p.hkv = hkv;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.block_shift = __builtin_ctz((unsigned)block_size);
+    p.per_row = hkv * (head_dim / 8);
+    p.tile_rows = std::max(1, kGatherChunks / p.per_row);
+    p.row_magic = (uint32_t)(((1ull << 32) + p.per_row - 1) / p.per_row);
+    p.err = err_flag;
+    const long long tiles = ((long long)total_k + p.tile_rows - 1) / p.tile_rows;
+    const int grid = (int)std::min<long long>(tiles, (long long)device_sm_count() * kGatherBlocks);
+    if (head_dim == 128) gather_fp8_kernel<128><<<grid, kGatherThreads, 0, stream>>>(p);
+    else gather_fp8_kernel<64><<<grid, kGatherThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_failure(e, "gather_kv_fp8 launch");
     count_launches(1);
