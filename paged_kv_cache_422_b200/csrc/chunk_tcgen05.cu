@@ -65,8 +65,8 @@ struct Roles {
     static constexpr int WARPS = FP8 ? 16 : 12;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
-    static constexpr int SMALL_REGS = FP8 ? 64 : 104;      // warps 0..3 and 12..15
-    static constexpr int SOFTMAX_REGS = FP8 ? 192 : 200;   // warps 4..11
+    static constexpr int SMALL_REGS = FP8 ? 80 : 104;      // warps 0..3 and 12..15
+    static constexpr int SOFTMAX_REGS = FP8 ? 176 : 200;   // warps 4..11
     static constexpr int READERS = 1 + 2 + 8 + (FP8 ? 4 : 0);  // of the unit ring
     // shared memory at head_dim 128: Q tiles and K/V tiles (bf16, ready for the MMAs) of 32 KB,
     // staged e4m3 tiles of 16 KB.  A tile takes 2 us from its copy's issue to its arrival, so
