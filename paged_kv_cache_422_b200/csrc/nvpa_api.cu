@@ -406,6 +406,9 @@ nvpa_status_t nvpa_gather_kv_fp8(void* dst, const void* cache, const uint8_t* sc
                              total_k, num_kv_heads, head_dim, num_blocks, block_size, err_flag, stream);
 }
 
+// Positions, rounded up to whole tiles, stay in 31 bits.
+constexpr int kMaxWindowContext = 1 << 30;
+
 // The checks that the windowed decode and the chunk attention share; *empty is set when
 // there is nothing to do.
 static nvpa_status_t check_window_call(const WindowCall& c, int cache_type, bool* empty) {
@@ -423,6 +426,7 @@ static nvpa_status_t check_window_call(const WindowCall& c, int cache_type, bool
     NVPA_REQUIRE(std::isfinite(c.scale), NVPA_ERR_INVALID_ARG, "softmax_scale not finite");
     NVPA_REQUIRE((long long)c.total_q * c.hq <= 0x7fffffffLL, NVPA_ERR_UNSUPPORTED,
                  "query rows times num_q_heads above 2^31-1");
+    NVPA_REQUIRE(c.max_context_len <= kMaxWindowContext, NVPA_ERR_UNSUPPORTED, "max_context_len above 2^30");
     if (c.batch == 0 || c.total_q == 0) {
         *empty = true;
         return NVPA_OK;
@@ -445,7 +449,8 @@ static nvpa_status_t check_window_call(const WindowCall& c, int cache_type, bool
 static bool window_sizes_ok(int hq, int hkv, int head_dim, int max_context_len, int window, int num_sinks,
                             int num_splits) {
     return hq > 0 && hkv > 0 && hq % hkv == 0 && hq / hkv <= 8 && (head_dim == 64 || head_dim == 128) &&
-           max_context_len >= 0 && window >= 0 && num_sinks >= 0 && num_splits >= 0;
+           max_context_len >= 0 && max_context_len <= kMaxWindowContext && window >= 0 && num_sinks >= 0 &&
+           num_splits >= 0;
 }
 
 size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,

@@ -171,3 +171,31 @@ def test_store_on_another_stream_and_in_a_graph(cuda_device):
     assert np.array_equal(kc.view(torch.uint8).cpu().numpy(), codes)
     assert np.array_equal(ks.cpu().numpy(), scales)
     assert np.array_equal(bits_of(k), bits)
+
+
+@pytest.mark.parametrize("lens,hkv,d,bs", [
+    ([300, 0, 41], 160, 64, 16),          # a row of more chunks than a block takes at once
+    ([5, 9], 128, 128, 16),
+    ([1] * 700, 1, 64, 16),               # many short sequences
+    ([20000], 1, 128, 256),
+])
+def test_gather_of_wide_rows_and_many_sequences(cuda_device, lens, hkv, d, bs):
+    dev = cuda_device
+    need = [-(-n // bs) for n in lens]
+    nb = sum(need) + 1
+    g = torch.Generator(device=dev).manual_seed(5)
+    codes = torch.randint(0, 127, (nb, bs, hkv, d), generator=g, device=dev, dtype=torch.uint8)
+    scales = torch.randint(100, 140, (nb, hkv, bs), generator=g, device=dev, dtype=torch.uint8)
+    order = torch.randperm(nb, generator=g, device=dev).int()
+    tables = torch.full((len(lens), max(need)), -3, dtype=torch.int32, device=dev)
+    at = 0
+    for b, k in enumerate(need):
+        tables[b, :k] = order[at:at + k]
+        at += k
+    cu = i32(np.concatenate([[0], np.cumsum(lens)]), dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out = nvpa.gather_kv_fp8(codes.view(torch.float8_e4m3fn), scales, tables, cu, sum(lens), err_flag=err)
+    assert err.item() == 0
+    full = codes.view(torch.float8_e4m3fn).float() * torch.exp2(scales.float() - 127).transpose(1, 2)[..., None]
+    want = torch.cat([full[tables[b, :need[b]].long()].flatten(0, 1)[:n] for b, n in enumerate(lens) if n])
+    assert torch.equal(out.float(), want)      # a code times a power of two is a bf16 value
