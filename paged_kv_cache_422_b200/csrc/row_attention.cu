@@ -868,20 +868,21 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // 16-key tiles per partition, from host-side bounds only (a captured call keeps its launches and
 // its workspace, and a sequence's partitions do not depend on the others' lengths).  `pairs`
 // row tiles times KV heads see `seen` tiles each at most.
-//  - Many pairs (more than an eighth of the resident warps): 22 tiles, many rounds of items
-//    whose varying lengths even the rounds out (64 contexts of 0.5 to 4 k keys in 8 bits: 73 us;
-//    28 tiles 77, 18 tiles 80, 37 tiles 84).
-//  - Few long ones: as many partitions as keep every item in one round, less a tenth for
-//    lengths that the host does not know (8 contexts of 32 k keys: 24 partitions each 107 us,
-//    27 109, 30, where a second round begins, 146, 64 124).
+//  - Up to a quarter as many pairs as warps: as many partitions as keep every item in one round,
+//    less a twelfth for lengths that the host does not know (8 contexts of 32 k keys in 8 bits: 24
+//    partitions each 107 us, 27 109, 30, where a second round begins, 146, 64 124; 40 of 4 k: 5
+//    69 us, 4 75, 8 83, 12 82; 40 of 0.5 to 4 k: 5 53 us, 12 60).
+//  - More: 22 tiles, many rounds of items whose varying lengths even the rounds out (64 contexts
+//    of 0.5 to 4 k keys: 73 us; 28 tiles 77, 18 tiles 80, 37 tiles 84; 56: 67 us, 3 partitions
+//    75).
 // Four tiles at least: shorter items cost more than the warps they fill.
 constexpr long long row_resident_warps(int nt) { return 148LL * kRowWarps * (nt == 1 ? 3 : 2); }   // on a B200
 int row_chunk_tiles(long long pairs, long long seen, int nt, int num_splits) {
     if (num_splits > 0) return (int)std::max(1LL, (seen + num_splits - 1) / num_splits);
     const long long warps = row_resident_warps(nt);
     long long chunk = 22;
-    if (pairs * 8 <= warps) {
-        const long long parts = std::max(1LL, warps * 9 / 10 / std::max(1LL, pairs));
+    const long long parts = warps * 11 / 12 / std::max(1LL, pairs);
+    if (parts >= 4) {
         chunk = std::max(4LL, (seen + parts - 1) / parts);
     }
     return (int)std::min(chunk, seen);
