@@ -481,9 +481,9 @@ nvpa_status_t nvpa_paged_decode_attention_window(
 
 // Which kernel a chunk call takes: few query rows per KV head (tokens times heads of its group)
 // go to the row kernel, which reads the keys once for 16 rows (24 of an e4m3 cache); more go to
-// the 128-row tiles.  (8 contexts of 8 k keys, 32 / 8 heads, e4m3 cache: 16 rows 49 us by rows
-// and 72 by tiles, 20 rows 65 and 72, 32 rows 106 and 72; bf16 cache: 12 rows 65 and 62, 20 rows
-// 75 and 62.)
+// the 128-row tiles.  (8 contexts of 8 k keys, 32 / 8 heads, e4m3 cache: 16 rows 50 us by rows
+// and 71 by tiles, 20 rows 58 and 71, 32 rows in two passes 106 and 71; bf16 cache: 12 rows 65
+// and 62, 20 rows 75 and 62.)
 constexpr int kRowKernelRows = 16, kRowKernelRowsE4m3 = 24;
 static bool chunk_on_tiles(int max_seqlen_q, int num_q_heads, int num_kv_heads, bool e4m3) {
     return (long long)max_seqlen_q * (num_q_heads / num_kv_heads) > (e4m3 ? kRowKernelRowsE4m3 : kRowKernelRows);

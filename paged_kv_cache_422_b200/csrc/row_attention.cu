@@ -239,7 +239,13 @@ __device__ __forceinline__ float max_over_keys(float v) {   // lanes with the sa
 // A stage of a warp's ring: TILES 16-key tiles that are worked on together.
 template <int D, bool FP8, int NT>
 struct RowStage {
-    static constexpr int TILES = FP8 && NT <= 2 ? 2 : 1;
+    static constexpr int TILES = FP8 ? 2 : 1;
+    // The Q fragments of 24 rows live in shared memory: beside 48 registers of them only one tile
+    // at a time would fit the register file, and two independent tiles hide the latency of 8
+    // warps per SM (5 draft tokens, 4 heads per group, 30 contexts of 8 k: 157 us, one tile 193;
+    // 16 rows one tile at a time in 12 warps per SM: 179 us against 136).
+    static constexpr bool Q_SMEM = NT > 2;
+    static constexpr int Q_BYTES = Q_SMEM ? NT * (D / 16) * 32 * 8 : 0;
     static constexpr int ROW = FP8 ? D : 2 * D;             // bytes of a key's row
     static constexpr int CHUNKS = ROW / 16;
     static constexpr int KV = kTileKeys * ROW;              // K of a tile, then its V
@@ -445,7 +451,17 @@ row_attention_kernel(const RowParams p) {
     // ---------------- consume side ----------------
     int4 a = make_int4(0, 0, 0, 0), b = a;
     int hk = 0;                    // item being consumed
-    uint32_t qf[NT][KK][2];
+    uint32_t qf[Stage::Q_SMEM ? 1 : NT][Stage::Q_SMEM ? 1 : KK][2] = {};
+    uint2* const qs_mem = reinterpret_cast<uint2*>(smem + (size_t)kRowWarps * STAGES * (Stage::BYTES + 48) +
+                                                   warp * Stage::Q_BYTES) + lane;
+    auto q_frag = [&](int j, int k) {
+        if constexpr (Stage::Q_SMEM) return qs_mem[(j * KK + k) * 32];
+        else return make_uint2(qf[j][k][0], qf[j][k][1]);
+    };
+    auto set_q = [&](int j, int k, uint32_t x, uint32_t y) {
+        if constexpr (Stage::Q_SMEM) qs_mem[(j * KK + k) * 32] = make_uint2(x, y);
+        else qf[j][k][0] = x, qf[j][k][1] = y;
+    };
     float qs[NT][2];               // score factor of rows 8 j + 2 t + {0, 1}
     int pos[NT][2];                // their positions (-1: no such row)
     float o[NT][MT][4];
@@ -486,14 +502,15 @@ row_attention_kernel(const RowParams p) {
                 fac *= scale_value(eq);
 #pragma unroll
                 for (int i = 0; i < KK; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) qf[j][i][x] = pack_half2(bf16_lo(w[i][x]) * inv, bf16_hi(w[i][x]) * inv);
+                    set_q(j, i, pack_half2(bf16_lo(w[i][0]) * inv, bf16_hi(w[i][0]) * inv),
+                          pack_half2(bf16_lo(w[i][1]) * inv, bf16_hi(w[i][1]) * inv));
             } else {
 #pragma unroll
                 for (int i = 0; i < KK / 2; ++i) {   // 8 dims per chunk
                     const int c = 2 * t + (i & 1) + 8 * (i >> 1);
                     const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(src + c * 8)) : make_uint4(0, 0, 0, 0);
-                    qf[j][2 * i][0] = u.x; qf[j][2 * i][1] = u.y; qf[j][2 * i + 1][0] = u.z; qf[j][2 * i + 1][1] = u.w;
+                    set_q(j, 2 * i, u.x, u.y);
+                    set_q(j, 2 * i + 1, u.z, u.w);
                 }
             }
 #pragma unroll
@@ -583,19 +600,26 @@ row_attention_kernel(const RowParams p) {
 #pragma unroll
             for (int i = 0; i < KK / 4; ++i) {
                 const int c = (KK / 4) * t + i;
+                uint4 lo[TILES], hi[TILES];
 #pragma unroll
                 for (int u = 0; u < TILES; ++u) {
                     const uint8_t* ks = sb + u * 2 * Stage::KV;
-                    const uint4 a0 = *reinterpret_cast<const uint4*>(ks + Stage::at(g, c));
-                    const uint4 a1 = *reinterpret_cast<const uint4*>(ks + Stage::at(g + 8, c));
-                    const uint32_t lo[4] = {a0.x, a0.y, a0.z, a0.w}, hi[4] = {a1.x, a1.y, a1.z, a1.w};
+                    lo[u] = *reinterpret_cast<const uint4*>(ks + Stage::at(g, c));
+                    hi[u] = *reinterpret_cast<const uint4*>(ks + Stage::at(g + 8, c));
+                }
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        uint32_t f[4];
-                        e4m3x4_to_half2(lo[y], f[0], f[2]);
-                        e4m3x4_to_half2(hi[y], f[1], f[3]);
+                for (int y = 0; y < 4; ++y) {
+                    uint32_t f[TILES][4];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) mma_f16(sc[u][j], f, qf[j][4 * i + y][0], qf[j][4 * i + y][1]);
+                    for (int u = 0; u < TILES; ++u) {
+                        e4m3x4_to_half2(y == 0 ? lo[u].x : y == 1 ? lo[u].y : y == 2 ? lo[u].z : lo[u].w, f[u][0], f[u][2]);
+                        e4m3x4_to_half2(y == 0 ? hi[u].x : y == 1 ? hi[u].y : y == 2 ? hi[u].z : hi[u].w, f[u][1], f[u][3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint2 q = q_frag(j, 4 * i + y);
+#pragma unroll
+                        for (int u = 0; u < TILES; ++u) mma_f16(sc[u][j], f[u], q.x, q.y);
                     }
                 }
             }
@@ -608,8 +632,9 @@ row_attention_kernel(const RowParams p) {
                 const uint32_t f0[4] = {a0.x, a1.x, a0.y, a1.y}, f1[4] = {a0.z, a1.z, a0.w, a1.w};
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    mma_bf16(sc[0][j], f0, qf[j][2 * i][0], qf[j][2 * i][1]);
-                    mma_bf16(sc[0][j], f1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+                    const uint2 q0 = q_frag(j, 2 * i), q1 = q_frag(j, 2 * i + 1);
+                    mma_bf16(sc[0][j], f0, q0.x, q0.y);
+                    mma_bf16(sc[0][j], f1, q1.x, q1.y);
                 }
             }
         }
@@ -823,7 +848,7 @@ row_attention_kernel(const RowParams p) {
 // ------------------------------------------------------------------------------------
 template <int D, bool FP8, int NT>
 constexpr int row_smem() {
-    return kRowWarps * kRowStages * (RowStage<D, FP8, NT>::BYTES + 48);
+    return kRowWarps * (kRowStages * (RowStage<D, FP8, NT>::BYTES + 48) + RowStage<D, FP8, NT>::Q_BYTES);
 }
 
 template <int D, bool FP8, int NT>
