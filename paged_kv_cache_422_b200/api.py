@@ -327,17 +327,42 @@ def lse_combine(o_parts, lse_parts, out=None, lse_out=None, stream=None, return_
 # These calls are a few microseconds of GPU work at small sizes, so a well-formed call takes one
 # comparison per tensor; only a refused one goes through the checks that name the fault.
 
-def _expect(t, dtype, name, ndim, index, contiguous=True):
-    """Refuse t unless it is a `dtype` tensor of ndim dimensions (None: any) on CUDA device
-    `index`."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
-            and t.get_device() == index and t.is_contiguous()):
+def _expect(t, dtype, name, shape, index):
+    """Refuse t unless it is a contiguous `dtype` tensor of this shape (a number: of that many
+    dimensions) on CUDA device `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous() and (t.shape == shape or t.dim() == shape)):
         return
+    ndim = shape if isinstance(shape, int) else len(shape)
     _need(t, dtype, name, ndim)
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if contiguous:
-        _contig(t, name)
+    if ndim != shape and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    _contig(t, name)
+
+
+def _expect_rows(t, name, shape, index):
+    """As _expect for bf16 rows [N, Hkv, D] whose token stride may exceed Hkv * D."""
+    if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
+        return
+    _need(t, _BF16, name, 3)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if shape[0] and (t.stride(2) != 1 or t.stride(1) != shape[2]):
+        raise ValueError(f"{name}: heads and dims of a token must be contiguous")
+
+
+def _flag_ptr(err_flag, index):
+    if err_flag is None:
+        return None
+    _need(err_flag, _I32, "err_flag")
+    if err_flag.get_device() != index:
+        raise ValueError(f"err_flag is on {err_flag.device}, expected cuda:{index}")
+    return err_flag.data_ptr()
 
 
 def _raw_stream(index, stream):
@@ -361,7 +386,7 @@ def _empty(shape, dtype, index, stream):
 def _call(name, index, *args):
     """Call a C entry point with device `index` current."""
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args)
     else:
         with torch.cuda.device(index):
@@ -369,18 +394,16 @@ def _call(name, index, *args):
     check(st, name)
 
 
-def _fp8_cache(cache, scales, cache_name="cache", scales_name="scales", index=None):
+def _fp8_cache(cache, scales, cache_name="cache", scales_name="scales"):
     """(dimensions, device index) of one e4m3 pool [num_blocks, block_size, Hkv, D] with its
     scale bytes [num_blocks, Hkv, block_size]."""
-    if index is None:
-        _need(cache, _FP8, cache_name, 4)
-        index = cache.get_device()
-    _expect(cache, _FP8, cache_name, 4, index)
-    _expect(scales, _U8, scales_name, 3, index)
-    nb, bs, hkv, d = cache.shape
-    if scales.shape != (nb, hkv, bs):
-        raise ValueError(f"{scales_name} must be [{nb}, {hkv}, {bs}], got {tuple(scales.shape)}")
-    return (nb, bs, hkv, d), index
+    _need(cache, _FP8, cache_name, 4)
+    index = cache.get_device()
+    _contig(cache, cache_name)
+    dims = cache.shape
+    nb, bs, hkv, _ = dims
+    _expect(scales, _U8, scales_name, (nb, hkv, bs), index)
+    return dims, index
 
 
 def _any_cache(k_cache, v_cache, k_scales, v_scales):
@@ -390,11 +413,11 @@ def _any_cache(k_cache, v_cache, k_scales, v_scales):
     if k_scales is None:
         dims = _cache_dims(k_cache, v_cache)
         index = k_cache.get_device()
-        _expect(v_cache, _BF16, "v_cache", 4, index)
+        _expect(v_cache, _BF16, "v_cache", dims, index)
         return dims, NVPA_CACHE_BF16, index
     dims, index = _fp8_cache(k_cache, k_scales, "k_cache", "k_scales")
-    if _fp8_cache(v_cache, v_scales, "v_cache", "v_scales", index)[0] != dims:
-        raise ValueError("k_cache and v_cache shapes differ")
+    _expect(v_cache, _FP8, "v_cache", dims, index)
+    _expect(v_scales, _U8, "v_scales", k_scales.shape, index)
     return dims, NVPA_CACHE_E4M3, index
 
 
@@ -407,22 +430,15 @@ def store_kvcache_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, 
     (nb, bs, hkv, d), _, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
     if k_scales is None:
         raise TypeError("k_scales and v_scales are required")
-    _expect(k, _BF16, "k", 3, index, contiguous=False)
-    _expect(v, _BF16, "v", 3, index, contiguous=False)
     _expect(slot_mapping, _I32, "slot_mapping", 1, index)
     n = slot_mapping.shape[0]
-    for name, t in (("k", k), ("v", v)):
-        if t.shape != (n, hkv, d):
-            raise ValueError(f"{name} must be [{n}, {hkv}, {d}], got {tuple(t.shape)}")
-        if n and not t.is_contiguous() and (t.stride(2) != 1 or t.stride(1) != d):
-            raise ValueError(f"{name}: heads and dims of a token must be contiguous")
-    if err_flag is not None:
-        _expect(err_flag, _I32, "err_flag", None, index)
+    _expect_rows(k, "k", (n, hkv, d), index)
+    _expect_rows(v, "v", (n, hkv, d), index)
     _call(
         "nvpa_store_kvcache_fp8", index,
         k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0), k_cache.data_ptr(),
         v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(),
-        n, hkv, d, nb, bs, _ptr(err_flag), _raw_stream(index, stream))
+        n, hkv, d, nb, bs, _flag_ptr(err_flag, index), _raw_stream(index, stream))
 
 
 def gather_kv_fp8(cache, scales, block_tables, cu_seqlens_k, total_k, out=None, err_flag=None,
@@ -439,20 +455,16 @@ def gather_kv_fp8(cache, scales, block_tables, cu_seqlens_k, total_k, out=None, 
     if out is None:
         out = _empty(shape, _BF16, index, stream)
     else:
-        _expect(out, _BF16, "out", 3, index)
-        if out.shape != shape:
-            raise ValueError(f"out must be {list(shape)}, got {tuple(out.shape)}")
-    if err_flag is not None:
-        _expect(err_flag, _I32, "err_flag", None, index)
+        _expect(out, _BF16, "out", shape, index)
     _call(
         "nvpa_gather_kv_fp8", index,
         out.data_ptr(), cache.data_ptr(), scales.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], cu_seqlens_k.data_ptr(), batch, total_k, hkv, d, nb, bs,
-        _ptr(err_flag), _raw_stream(index, stream))
+        _flag_ptr(err_flag, index), _raw_stream(index, stream))
     return out
 
 
-def _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, rows_name):
+def _window_outputs(q, d, index, stream, out, lse, return_lse):
     """Checks of q and the outputs; (query rows, query heads, out, lse)."""
     _expect(q, _BF16, "q", 3, index)
     n, hq, dq = q.shape
@@ -461,13 +473,9 @@ def _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, rows_name):
     if out is None:
         out = _empty(q.shape, _BF16, index, stream)
     else:
-        _expect(out, _BF16, "out", 3, index)
-        if out.shape != q.shape:
-            raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        _expect(out, _BF16, "out", q.shape, index)
     if lse is not None:
-        _expect(lse, torch.float32, "lse", 2, index)
-        if lse.shape != (n, hq):
-            raise ValueError(f"lse must be [{rows_name}, Hq] = [{n}, {hq}], got {tuple(lse.shape)}")
+        _expect(lse, torch.float32, "lse", (n, hq), index)
     elif return_lse:
         lse = _empty((n, hq), torch.float32, index, stream)
     return n, hq, out, lse
@@ -501,15 +509,11 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
     [B, Hq, D] bf16, one query per sequence, which sees the last `window` keys (0: all) and
     the first `num_sinks`."""
     (nb, bs, hkv, d), kind, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
-    b, hq, out, lse = _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, "B")
+    b, hq, out, lse = _window_outputs(q, d, index, stream, out, lse, return_lse)
     _expect(block_tables, _I32, "block_tables", 2, index)
-    _expect(context_lens, _I32, "context_lens", 1, index)
+    _expect(context_lens, _I32, "context_lens", (b,), index)
     if block_tables.shape[0] != b:
         raise ValueError("block_tables: batch differs from q's")
-    if context_lens.shape[0] != b:
-        raise ValueError("context_lens: batch differs from q's")
-    if err_flag is not None:
-        _expect(err_flag, _I32, "err_flag", None, index)
     ws, ws_bytes, workspace = _workspace(
         workspace, index, stream, paged_decode_window_workspace_size, b, hq, hkv, d, max_context_len, bs,
         window, num_sinks, num_splits)
@@ -519,7 +523,7 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
         _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
         context_lens.data_ptr(), b, hq, hkv, d, nb, bs, int(max_context_len),
         float(softmax_scale), int(window), int(num_sinks), int(num_splits), ws, ws_bytes,
-        _ptr(err_flag), _raw_stream(index, stream))
+        _flag_ptr(err_flag, index), _raw_stream(index, stream))
     return (out, lse) if return_lse else out
 
 
@@ -540,15 +544,13 @@ def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_len
     ones included, in a bf16 cache, or an e4m3 one with its k_scales / v_scales; a query sees
     the last `window` keys up to its own (0: all) and the first `num_sinks`."""
     (nb, bs, hkv, d), kind, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
-    total_q, hq, out, lse = _window_outputs(q, hkv, d, index, stream, out, lse, return_lse, "total_q")
+    total_q, hq, out, lse = _window_outputs(q, d, index, stream, out, lse, return_lse)
     _expect(block_tables, _I32, "block_tables", 2, index)
     _expect(cu_seqlens_q, _I32, "cu_seqlens_q", 1, index)
     _expect(context_lens, _I32, "context_lens", 1, index)
     batch = context_lens.shape[0]
     if block_tables.shape[0] != batch or cu_seqlens_q.shape[0] != batch + 1:
         raise ValueError("block_tables, cu_seqlens_q and context_lens disagree about the batch")
-    if err_flag is not None:
-        _expect(err_flag, _I32, "err_flag", None, index)
     ws, ws_bytes, workspace = _workspace(
         workspace, index, stream, chunk_attention_workspace_size, batch, total_q, hq, hkv, d, max_seqlen_q,
         max_context_len, bs, window, num_sinks, num_splits)
@@ -558,5 +560,5 @@ def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_len
         _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
         cu_seqlens_q.data_ptr(), context_lens.data_ptr(), batch, total_q, int(max_seqlen_q),
         int(max_context_len), hq, hkv, d, nb, bs, float(softmax_scale), int(window),
-        int(num_sinks), int(num_splits), ws, ws_bytes, _ptr(err_flag), _raw_stream(index, stream))
+        int(num_sinks), int(num_splits), ws, ws_bytes, _flag_ptr(err_flag, index), _raw_stream(index, stream))
     return (out, lse) if return_lse else out

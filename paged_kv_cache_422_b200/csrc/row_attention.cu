@@ -70,7 +70,7 @@ struct RowParams {
     int max_blocks, num_blocks, block_size, block_shift;
     int max_ctx;
     int window, sinks;           // window 0: none
-    int planned;                 // items come from the plan kernel (always for chunks)
+    int planned;                 // items come from the plan kernel
     int tok;                     // query tokens per row tile
     int row_tiles;               // row tiles of the longest chunk
     int chunk;                   // 16-key tiles per partition
@@ -140,7 +140,7 @@ __device__ __forceinline__ int full_parts(const RowParams& p, const RowTile& t) 
 }
 
 // ------------------------------------------------------------------------------------
-// plan of chunk calls: context lengths -> items, full partitions first, then the shorter ones, longest
+// plan: context lengths -> items, full partitions first, then the shorter ones, longest
 // first (as the decode plan orders them)
 // ------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
@@ -288,11 +288,11 @@ row_attention_kernel(const RowParams p) {
 
     const int nwarps = gridDim.x * kRowWarps;
     int nx_item = blockIdx.x * kRowWarps + warp;
-    // A decode call whose items fit one round has no plan kernel, which would cost 5 us of its
-    // 20 to 100: every CTA counts the sequences' partitions itself, a sequence per thread.  Items
-    // are the full partitions of all sequences, then the shorter last ones, each for every KV
-    // head.  (With several rounds the plan's order and dynamic claims are worth more than its
-    // time: 64 contexts of 0.5 to 4 k keys 72 us with it, 78 without.)
+    // A call whose items fit one round has no plan kernel, which would cost 5 us of its 15 to 100:
+    // every CTA counts the row tiles' partitions itself, a row tile per thread.  Items are the
+    // full partitions of all row tiles, then the shorter last ones, each for every KV head.  (With
+    // several rounds the plan's order and dynamic claims are worth more than its time: 64 contexts
+    // of 0.5 to 4 k keys 72 us with it, 78 without.)
     __shared__ int s_full[kRowWarps * 32], s_rest[kRowWarps * 32], s_scan[32];
     int total_items = 0, total_full = 0;
     if (p.planned) {
@@ -300,7 +300,7 @@ row_attention_kernel(const RowParams p) {
         total_items = __ldcg(p.counter + 1);
     } else {
         int full = 0, rest = 0, total_rest = 0;
-        if ((int)threadIdx.x < p.batch) {
+        if ((int)threadIdx.x < p.batch * p.row_tiles) {
             const RowTile r = row_tile(p, threadIdx.x, blockIdx.x == 0);
             full = full_parts(p, r);
             rest = r.ns - full;
@@ -310,7 +310,7 @@ row_attention_kernel(const RowParams p) {
         __syncthreads();
         total_items = (total_full + total_rest) * p.hkv;
     }
-    // item c (of one KV head) without a plan: its sequence is the last one with at most c
+    // item c (of one KV head) without a plan: its row tile is the last one with at most c
     // partitions before it
     auto find = [&](int c) {
         const bool rest = c >= total_full;
@@ -321,7 +321,7 @@ row_attention_kernel(const RowParams p) {
         for (int w = 0; w < kRowWarps; ++w) i += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= k));
         const RowTile r = row_tile(p, i, false);
         const int s = rest ? r.ns - 1 : k - before[i];
-        it_a = make_int4(i, s | (r.ns << 16), i, 1);
+        it_a = make_int4(r.b, s | (r.ns << 16), r.q0, r.ntok);
         it_b = make_int4(r.p0, s * p.chunk, min(r.tiles, (s + 1) * p.chunk), 0);
     };
     auto real_tile = [&](int v) { return v < it_r.head ? v : v + it_r.skip; };
@@ -530,7 +530,7 @@ row_attention_kernel(const RowParams p) {
 
     auto epilogue = [&]() {
         const int s = a.y & 0xffff, ns = a.y >> 16;
-        if (!p.planned && s == 0 && hk == 0 && lane == 0) p.nsplit[a.x] = ns;   // for the combine
+        if (!p.planned && s == 0 && hk == 0 && lane == 0) p.nsplit[a.z] = ns;   // for the combine
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -900,11 +900,14 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 //  - More: 22 tiles, many rounds of items whose varying lengths even the rounds out (64 contexts
 //    of 0.5 to 4 k keys: 73 us; 28 tiles 77, 18 tiles 80, 37 tiles 84; 56: 67 us, 3 partitions
 //    75).
-// Four tiles at least: shorter items cost more than the warps they fill.
+// Four tiles at least: shorter items cost more than the warps they fill; and up to 8 tiles stay
+// whole, since that saves the combine and a chunk's plan (one context of 128 keys 13.7 us, two
+// partitions 14.7; 4 chunks of 5 tokens at 128 keys 17.5 and 20.1, at 256 keys 23.4 and 20.1).
 constexpr long long row_resident_warps(int nt) { return 148LL * kRowWarps * (nt == 1 ? 3 : 2); }   // on a B200
 int row_chunk_tiles(long long pairs, long long seen, int nt, int num_splits) {
     if (num_splits > 0) return (int)std::max(1LL, (seen + num_splits - 1) / num_splits);
     const long long warps = row_resident_warps(nt);
+    if (seen <= 8) return (int)seen;
     long long chunk = 22;
     const long long parts = warps * 11 / 12 / std::max(1LL, pairs);
     if (parts >= 4) {
@@ -992,7 +995,9 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     p.window = c.window >= c.max_context_len ? 0 : c.window;
     p.sinks = std::min(c.num_sinks, c.max_context_len);
     p.max_entries = (int)(r.tiles * r.s_max);
-    p.planned = c.cu_seqlens_q != nullptr || c.batch > kRowWarps * 32 ||
+    // (a chunk call with partitions is planned: the combine needs to know the rows that no
+    // sequence owns)
+    p.planned = (c.cu_seqlens_q != nullptr && r.s_max > 1) || (long long)c.batch * r.row_tiles > kRowWarps * 32 ||
                 r.tiles * r.s_max * c.hkv > row_resident_warps(r.nt);
     p.tok = r.tok;
     p.row_tiles = r.row_tiles;
