@@ -474,9 +474,11 @@ size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int n
  *   num_splits      0 = automatic; n > 0 = at most n partitions of what a query can see.
  *   workspace       at least nvpa_paged_decode_window_workspace_size(...) bytes, 256-byte
  *                   aligned; calls that share a workspace must not overlap.
+ *   max_context_len at most 2^30 (NVPA_ERR_UNSUPPORTED above).
  *   other arguments, out, lse and errors as for nvpa_paged_decode_attention.
  * The softmax weights are rounded to 16 significant bits (bf16 cache) or 11 (e4m3 cache)
- * before the product with the values; sums are float32.
+ * before the product with the values; sums are float32.  A sequence's result depends on its own
+ * rows and on the call's host-side arguments only, not on the other sequences.
  */
 nvpa_status_t nvpa_paged_decode_attention_window(
     void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,
@@ -502,7 +504,12 @@ size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_hea
  * context_lens[i] - Lq + r; which keys a position sees (causal, window, sinks), and which
  * block-table entries are read, is as for nvpa_paged_decode_attention_window.  When there
  * are few query rows the keys are cut into partitions that run in parallel and are merged
- * with their log-sum-exp weights.
+ * with their log-sum-exp weights.  Up to 16 query rows (tokens times query heads) per KV head,
+ * 24 over an e4m3 cache, run as the decode does; longer chunks on 128-row tensor-core tiles,
+ * whose softmax weights are rounded to 8 significant bits (bf16).  Keys that no query row of the
+ * call sees never show in a result, whatever their rows hold; a key that some of a sequence's
+ * query rows see may, where its value is not finite, show in that sequence's other rows too
+ * (as 0 times it).
  *
  *   out             bf16 [total_q, num_q_heads, head_dim] (written); rows from
  *                   cu_seqlens_q[batch] on are left as they are.

@@ -374,13 +374,14 @@ def _raw_stream(index, stream):
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, index, stream):
-    """Memory for a call on `stream`, from that stream's pool: a workspace that is freed at
-    return, or memory that work queued elsewhere still uses, is then never handed out early."""
+def _empty(like, shape, dtype, stream):
+    """Memory for a call on `stream` and `like`'s device, from that stream's pool: a workspace
+    that is freed at return, or memory that work queued elsewhere still uses, is then never handed
+    out early."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _call(name, index, *args):
@@ -453,7 +454,7 @@ def gather_kv_fp8(cache, scales, block_tables, cu_seqlens_k, total_k, out=None, 
     total_k = int(total_k)
     shape = (total_k, hkv, d)
     if out is None:
-        out = _empty(shape, _BF16, index, stream)
+        out = _empty(cache, shape, _BF16, stream)
     else:
         _expect(out, _BF16, "out", shape, index)
     _call(
@@ -471,20 +472,20 @@ def _window_outputs(q, d, index, stream, out, lse, return_lse):
     if dq != d:
         raise ValueError("q head_dim differs from the cache's")
     if out is None:
-        out = _empty(q.shape, _BF16, index, stream)
+        out = _empty(q, q.shape, _BF16, stream)
     else:
         _expect(out, _BF16, "out", q.shape, index)
     if lse is not None:
         _expect(lse, torch.float32, "lse", (n, hq), index)
     elif return_lse:
-        lse = _empty((n, hq), torch.float32, index, stream)
+        lse = _empty(q, (n, hq), torch.float32, stream)
     return n, hq, out, lse
 
 
-def _workspace(workspace, index, stream, size, *args):
+def _workspace(workspace, like, index, stream, size, *args):
     """A workspace of size(*args) bytes, or the caller's; (pointer, bytes, tensor)."""
     if workspace is None:
-        workspace = _empty(size(*args), _U8, index, stream)
+        workspace = _empty(like, size(*args), _U8, stream)
     elif not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
     elif workspace.get_device() != index:
@@ -515,8 +516,8 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
     if block_tables.shape[0] != b:
         raise ValueError("block_tables: batch differs from q's")
     ws, ws_bytes, workspace = _workspace(
-        workspace, index, stream, paged_decode_window_workspace_size, b, hq, hkv, d, max_context_len, bs,
-        window, num_sinks, num_splits)
+        workspace, q, index, stream, paged_decode_window_workspace_size, b, hq, hkv, d,
+        max_context_len, bs, window, num_sinks, num_splits)
     _call(
         "nvpa_paged_decode_attention_window", index,
         out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind,
@@ -552,13 +553,14 @@ def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_len
     if block_tables.shape[0] != batch or cu_seqlens_q.shape[0] != batch + 1:
         raise ValueError("block_tables, cu_seqlens_q and context_lens disagree about the batch")
     ws, ws_bytes, workspace = _workspace(
-        workspace, index, stream, chunk_attention_workspace_size, batch, total_q, hq, hkv, d, max_seqlen_q,
-        max_context_len, bs, window, num_sinks, num_splits)
+        workspace, q, index, stream, chunk_attention_workspace_size, batch, total_q, hq, hkv, d,
+        max_seqlen_q, max_context_len, bs, window, num_sinks, num_splits)
     _call(
         "nvpa_chunk_attention", index,
         out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind,
         _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
         cu_seqlens_q.data_ptr(), context_lens.data_ptr(), batch, total_q, int(max_seqlen_q),
         int(max_context_len), hq, hkv, d, nb, bs, float(softmax_scale), int(window),
-        int(num_sinks), int(num_splits), ws, ws_bytes, _flag_ptr(err_flag, index), _raw_stream(index, stream))
+        int(num_sinks), int(num_splits), ws, ws_bytes, _flag_ptr(err_flag, index),
+        _raw_stream(index, stream))
     return (out, lse) if return_lse else out

@@ -12,14 +12,19 @@
 // byte for G query heads per KV head).  The products are small matrix products over the G
 // heads, so they go to warp-level MMAs with the keys as the M dimension and the query rows
 // as N = 8: S^T[16 keys, 8 rows] = K Q^T and O^T[D, 8 rows] += V^T P^T.  With CUDA-core
-// products the e4m3 cache's instructions per byte would bound the kernel; with MMAs 16 keys
-// take about 300 warp instructions for either cache and any G up to 8.  (tcgen05 needs M =
-// 64 or 128 rows of accumulators in TMEM per product, a single warp's stream of keys has no
-// use for it.)
+// products the e4m3 cache's instructions per byte would bound the kernel; with MMAs 32 keys of
+// it take about 670 warp instructions for any G up to 8, a third of them the conversion of its
+// codes.  (tcgen05 needs M = 64 or 128 rows of accumulators in TMEM per product, a single
+// warp's stream of keys has no use for it.)
+// Measured: 8 contexts of 32 k keys, 32 / 8 heads of 128, e4m3 cache: 104 us, 5.2 TB/s (0.80 of
+// the copy bandwidth; the marginal rate of more contexts is 6.3 TB/s, the rest is the start of
+// the streams, the merge and the launches); 256 contexts in a window of 1024 keys, bf16 cache:
+// 192 us, 5.5 TB/s; a context of 4 k keys alone 15 us.
 //
 // Layout.  Every warp is an independent worker: it takes items (KV head, row tile, range of
-// 16-key tiles of one sequence) and streams their K and V through its own ring of shared
-// memory stages with 16-byte cp.async copies.  Rows that no query row of the item sees are
+// 16-key tiles of one sequence) and streams their K and V through its own ring of two shared
+// memory stages (of two tiles, e4m3) with 16-byte cp.async copies.  Chunks of up to 24 rows per
+// KV head (16 over a bf16 cache) take 2 or 3 such N = 8 row groups in one pass over the keys.  Rows that no query row of the item sees are
 // zero-filled and never read, and neither are the block-table entries of blocks without a
 // visible key: blocks that fell out of the window may be freed.  A row's 16-byte chunks are
 // XOR-swizzled by its key so that the fragment loads below hit all banks.
@@ -408,8 +413,8 @@ row_attention_kernel(const RowParams p) {
             const uint32_t sd = (uint32_t)(st * Stage::BYTES);
 #pragma unroll
             for (int u = 0; u < TILES; ++u) {
-                const size_t off = ((size_t)it_blk[u] * p.block_size + (tile[u] * kTileKeys & (p.block_size - 1))) * row_bytes +
-                                   (size_t)it_hk * Stage::ROW + lane_off;
+                const size_t slot = (size_t)it_blk[u] * p.block_size + (tile[u] * kTileKeys & (p.block_size - 1));
+                const size_t off = slot * row_bytes + (size_t)it_hk * Stage::ROW + lane_off;
                 const uint8_t* kg = static_cast<const uint8_t*>(p.k_cache) + off;
                 const uint8_t* vg = static_cast<const uint8_t*>(p.v_cache) + off;
                 const uint32_t kd = sd + u * 2 * Stage::KV;
@@ -435,7 +440,8 @@ row_attention_kernel(const RowParams p) {
                     const int u = lane >> 1;
                     const size_t so = ((size_t)(u ? it_blk[TILES - 1] : it_blk[0]) * p.hkv + it_hk) * p.block_size +
                                       ((u ? tile[1] : tile[0]) * kTileKeys & (p.block_size - 1));
-                    cp_async16_to(wbase + sd + Stage::SCALES + lane * 16, ((lane & 1) ? p.v_scales : p.k_scales) + so, 16);
+                    cp_async16_to(wbase + sd + Stage::SCALES + lane * 16,
+                                  ((lane & 1) ? p.v_scales : p.k_scales) + so, 16);
                 }
             }
             if (lane == 0)
@@ -485,8 +491,9 @@ row_attention_kernel(const RowParams p) {
                 uint32_t w[KK][2];
 #pragma unroll
                 for (int i = 0; i < KK / 4; ++i) {   // 16 dims per 16-byte chunk of codes
-                    const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(src + ((KK / 4) * t + i) * 16)) : make_uint4(0, 0, 0, 0);
-                    const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(src + ((KK / 4) * t + i) * 16) + 1) : make_uint4(0, 0, 0, 0);
+                    const uint4* from = reinterpret_cast<const uint4*>(src + ((KK / 4) * t + i) * 16);
+                    const uint4 u = ok ? __ldg(from) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = ok ? __ldg(from + 1) : make_uint4(0, 0, 0, 0);
                     w[4 * i][0] = u.x; w[4 * i][1] = u.y; w[4 * i + 1][0] = u.z; w[4 * i + 1][1] = u.w;
                     w[4 * i + 2][0] = v.x; w[4 * i + 2][1] = v.y; w[4 * i + 3][0] = v.z; w[4 * i + 3][1] = v.w;
                 }
@@ -600,20 +607,22 @@ row_attention_kernel(const RowParams p) {
 #pragma unroll
             for (int i = 0; i < KK / 4; ++i) {
                 const int c = (KK / 4) * t + i;
-                uint4 lo[TILES], hi[TILES];
+                uint32_t lo[TILES][4], hi[TILES][4];
 #pragma unroll
                 for (int u = 0; u < TILES; ++u) {
                     const uint8_t* ks = sb + u * 2 * Stage::KV;
-                    lo[u] = *reinterpret_cast<const uint4*>(ks + Stage::at(g, c));
-                    hi[u] = *reinterpret_cast<const uint4*>(ks + Stage::at(g + 8, c));
+                    const uint4 a0 = *reinterpret_cast<const uint4*>(ks + Stage::at(g, c));
+                    const uint4 a1 = *reinterpret_cast<const uint4*>(ks + Stage::at(g + 8, c));
+                    lo[u][0] = a0.x; lo[u][1] = a0.y; lo[u][2] = a0.z; lo[u][3] = a0.w;
+                    hi[u][0] = a1.x; hi[u][1] = a1.y; hi[u][2] = a1.z; hi[u][3] = a1.w;
                 }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     uint32_t f[TILES][4];
 #pragma unroll
                     for (int u = 0; u < TILES; ++u) {
-                        e4m3x4_to_half2(y == 0 ? lo[u].x : y == 1 ? lo[u].y : y == 2 ? lo[u].z : lo[u].w, f[u][0], f[u][2]);
-                        e4m3x4_to_half2(y == 0 ? hi[u].x : y == 1 ? hi[u].y : y == 2 ? hi[u].z : hi[u].w, f[u][1], f[u][3]);
+                        e4m3x4_to_half2(lo[u][y], f[u][0], f[u][2]);
+                        e4m3x4_to_half2(hi[u][y], f[u][1], f[u][3]);
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
@@ -680,7 +689,8 @@ row_attention_kernel(const RowParams p) {
                 for (int u = 0; u < TILES; ++u)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint32_t seen = seen_keys(key0[u], pos[j][x], p.window, p.sinks) & ((uint32_t)meta.z >> (16 * u));
+                        const uint32_t seen = seen_keys(key0[u], pos[j][x], p.window, p.sinks) &
+                                              ((uint32_t)meta.z >> (16 * u));
                         if (!((seen >> g) & 1)) sc[u][j][x] = ew[u][j][x] = -INFINITY;
                         if (!((seen >> (g + 8)) & 1)) sc[u][j][2 + x] = ew[u][j][2 + x] = -INFINITY;
                     }
