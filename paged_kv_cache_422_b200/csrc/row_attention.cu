@@ -537,7 +537,7 @@ row_attention_kernel(const RowParams p) {
 
     auto epilogue = [&]() {
         const int s = a.y & 0xffff, ns = a.y >> 16;
-        if (!p.planned && s == 0 && hk == 0 && lane == 0) p.nsplit[a.z] = ns;   // for the combine
+        if (!p.planned && s == 0 && hk == 0 && lane < a.w) p.nsplit[a.z + lane] = ns;   // for the combine
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -1005,9 +1005,7 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     p.window = c.window >= c.max_context_len ? 0 : c.window;
     p.sinks = std::min(c.num_sinks, c.max_context_len);
     p.max_entries = (int)(r.tiles * r.s_max);
-    // (a chunk call with partitions is planned: the combine needs to know the rows that no
-    // sequence owns)
-    p.planned = (c.cu_seqlens_q != nullptr && r.s_max > 1) || (long long)c.batch * r.row_tiles > kRowWarps * 32 ||
+    p.planned = (long long)c.batch * r.row_tiles > kRowWarps * 32 ||
                 r.tiles * r.s_max * c.hkv > row_resident_warps(r.nt);
     p.tok = r.tok;
     p.row_tiles = r.row_tiles;
@@ -1020,6 +1018,10 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_failure(e, "row attention plan launch");
         count_launches(1);
+    } else if (c.cu_seqlens_q != nullptr && r.s_max > 1) {
+        // rows that no sequence owns have no partitions (the workers write the others' counts)
+        e = cudaMemsetAsync(p.nsplit, 0, sizeof(int32_t) * (size_t)c.total_q, stream);
+        if (e != cudaSuccess) return cuda_failure(e, "row attention memset");
     }
     const long long max_items = r.tiles * r.s_max * c.hkv;
     const bool fp8 = c.k_scales != nullptr;
