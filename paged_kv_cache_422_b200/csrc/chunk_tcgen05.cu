@@ -329,58 +329,6 @@ __device__ __forceinline__ void mask_columns(uint32_t (&sv)[kKeys], int base, in
     }
 }
 
-// 16 e4m3 codes times 2^(byte - 127) as bf16.  The products are exact (4 significant bits), so
-// the upper halves of their float32 forms are their bf16 forms.  A scale that is an fp16 value
-// (2^-24 .. 2^15: rows of magnitude up to 2^-16 .. 2^24) goes through the mixed-precision FMA,
-// which widens and scales in one instruction: 4.3 ns per warp and 32-bit word against 6.2 for
-// conversion, multiplication and packing.
-struct RowScale {
-    uint16_t half;    // 0: outside fp16
-    float value;
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t byte) {
-    RowScale r;
-    r.value = scale_value(byte);
-    r.half = byte > 142 || byte < 103 ? 0 : (uint16_t)(byte >= 113 ? (byte - 112) << 10 : 1u << (byte - 103));
-    return r;
-}
-__device__ __forceinline__ uint32_t scale_half2(uint32_t h2, uint16_t f) {
-    float x, y;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "fma.rn.f32.f16 %0, a, %3, %4;\n\tfma.rn.f32.f16 %1, b, %3, %4;\n\t}"
-        : "=f"(x), "=f"(y) : "r"(h2), "h"(f), "f"(0.f));
-    return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-}
-__device__ __forceinline__ void widen16(const uint4& u, uint16_t f, uint4& lo, uint4& hi) {
-    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        e4m3x4_to_half2(in[i], w[2 * i], w[2 * i + 1]);
-        w[2 * i] = scale_half2(w[2 * i], f);
-        w[2 * i + 1] = scale_half2(w[2 * i + 1], f);
-    }
-    lo = make_uint4(w[0], w[1], w[2], w[3]);
-    hi = make_uint4(w[4], w[5], w[6], w[7]);
-}
-// The same for any scale.
-__device__ __forceinline__ void widen16_any(const uint4& u, float f, uint4& lo, uint4& hi) {
-    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h[2];
-        e4m3x4_to_half2(in[i], h[0], h[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h[k]));
-            w[2 * i + k] = pack_bf16x2(x.x * f, x.y * f);
-        }
-    }
-    lo = make_uint4(w[0], w[1], w[2], w[3]);
-    hi = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
 template <int D, bool FP8>
 __global__ void __launch_bounds__(Roles<FP8>::THREADS, 1)
 chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,

@@ -5,8 +5,8 @@
 // Both are bound by HBM bandwidth (3 bytes per value: 2 of bf16, 1 of e4m3), so each value
 // is loaded once with 16-byte loads and the row's maximum never leaves the registers: D / 16
 // lanes hold one row (16 values each), log2(D / 16) shuffles give its largest magnitude.
-// Measured with 8 heads of 128: 24594 tokens stored in 25.4 us (6.0 TB/s, 0.91 of the copy
-// bandwidth), 33 k rows read back in 21.3 us (5.0 TB/s; 204 k rows 5.7 TB/s).
+// Measured with 8 heads of 128: 24594 tokens stored in 25.2 us (6.0 TB/s, 0.92 of the copy
+// bandwidth), 33 k rows read back in 18.7 us (5.7 TB/s, 0.88).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -37,11 +37,18 @@ __device__ __forceinline__ uint32_t lane_amax(const uint32_t (&w)[8], bool& odd)
     return m;
 }
 
-// The 16 values of a lane as e4m3 codes, multiplied by inv = 2^-e (exact) first.
-__device__ __forceinline__ uint4 lane_codes(const uint32_t (&w)[8], float inv, bool odd) {
+// The 16 values of a lane as e4m3 codes, multiplied by 2^-e (exact; inv holds its bf16 bits)
+// first: the mixed-precision FMA unpacks and multiplies a bf16 value in one instruction.
+__device__ __forceinline__ uint4 lane_codes(const uint32_t (&w)[8], uint16_t inv, bool odd) {
     uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = pack_e4m3x2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+    for (int i = 0; i < 8; ++i) {
+        float x, y;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "fma.rn.f32.bf16 %0, a, %3, %4;\n\tfma.rn.f32.bf16 %1, b, %3, %4;\n\t}"
+            : "=f"(x), "=f"(y) : "r"(w[i]), "h"(inv), "f"(-0.f));   // (-0 keeps the sign of a zero)
+        h[i] = pack_e4m3x2(x, y);
+    }
     if (odd) {   // an infinity has no code: it is stored as NaN, like a NaN
         for (int i = 0; i < 8; ++i) {
             if ((w[i] & 0x7fffu) >= 0x7f80u) h[i] = (h[i] & 0xff00u) | kE4m3Nan;
@@ -100,8 +107,8 @@ __global__ void __launch_bounds__(256) store_fp8_kernel(const StoreFp8Params p) 
     if (slot < 0) return;
     const int kb = scale_byte(m >> 16), vb = scale_byte(m & 0xffffu);
     const size_t at = ((size_t)slot * p.hkv + h) * D + sub * 16;
-    *reinterpret_cast<uint4*>(p.k_cache + at) = lane_codes(kw, scale_value(254 - kb), kodd);
-    *reinterpret_cast<uint4*>(p.v_cache + at) = lane_codes(vw, scale_value(254 - vb), vodd);
+    *reinterpret_cast<uint4*>(p.k_cache + at) = lane_codes(kw, (uint16_t)((254 - kb) << 7), kodd);
+    *reinterpret_cast<uint4*>(p.v_cache + at) = lane_codes(vw, (uint16_t)((254 - vb) << 7), vodd);
     if (sub == 0) {
         const int blk = slot / p.block_size;
         const size_t sat = ((size_t)blk * p.hkv + h) * p.block_size + (slot - blk * p.block_size);
@@ -110,13 +117,14 @@ __global__ void __launch_bounds__(256) store_fp8_kernel(const StoreFp8Params p) 
     }
 }
 
-// A block takes tiles of whole rows, about kGatherChunks chunks of 8 codes (16 bytes of bf16
-// each, so that a warp's stores fill whole lines).  Reading a chunk hangs on three loads
+// A block takes tiles of whole rows, about kGatherChunks chunks of 16 codes (32 bytes of bf16,
+// one store where the destination is 32-byte aligned).  Reading a chunk hangs on three loads
 // (sequence, block id, codes), so the slots of the next tile's rows are looked up, a row per
 // thread, while this tile's codes are on their way.
-constexpr int kGatherThreads = 256, kGatherPer = 4, kGatherChunks = kGatherThreads * kGatherPer;
-// Blocks per SM: as many as fit (33 k rows of 8 heads of 128: 4 per SM 24.4 us, 6 23.5, 8 21.3,
-// unlimited 22.6).
+constexpr int kGatherThreads = 256, kGatherPer = 2, kGatherChunks = kGatherThreads * kGatherPer;
+// Blocks per SM: as many as fit.  (33 k rows of 8 heads of 128: 18.7 us; chunks of 8 codes, whose
+// address work is the same, 21.3, and with 4 or 6 blocks 24.4 and 23.5; four chunks a thread in
+// 6 blocks 19.1.)
 constexpr int kGatherBlocks = 8;
 
 struct GatherFp8Params {
@@ -126,7 +134,8 @@ struct GatherFp8Params {
     const int32_t* block_tables;
     const int32_t* cu;
     int max_blocks, batch, total_k, hkv, num_blocks, block_size, block_shift;
-    int per_row;           // chunks of a row, hkv * D / 8
+    int per_row;           // chunks of a row, hkv * D / 16
+    int dst_v8;            // dst is 32-byte aligned
     int tile_rows;
     uint32_t row_magic;    // ceil(2^32 / per_row): j / per_row = umulhi(j, row_magic) for j * per_row < 2^32
     int32_t* err;
@@ -134,7 +143,7 @@ struct GatherFp8Params {
 
 template <int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const GatherFp8Params p) {
-    constexpr int CPH = D / 8;                                // chunks per head
+    constexpr int CPH = D / 16;                               // chunks per head
     constexpr int kMaxRows = kGatherChunks / CPH;             // rows of a tile
     constexpr int kNoRow = -2, kZeroRow = -1;
     __shared__ int s_slot[2][kMaxRows];
@@ -165,24 +174,24 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Gather
     for (int buf = 0; row0 < p.total_k; buf ^= 1) {
         __syncthreads();
         const int n = min(p.tile_rows, p.total_k - row0) * p.per_row;
-        uint4* dst = reinterpret_cast<uint4*>(p.dst) + (size_t)row0 * p.per_row;
+        uint4* dst = reinterpret_cast<uint4*>(p.dst) + 2 * (size_t)row0 * p.per_row;
         // (one round, but for rows of more than kGatherChunks chunks)
         for (int base = 0; base < n; base += kGatherChunks) {
-            uint2 code[kGatherPer];
+            uint4 code[kGatherPer];
             uint32_t scale[kGatherPer];
             int slot[kGatherPer];
 #pragma unroll
             for (int k = 0; k < kGatherPer; ++k) {
                 const int j = base + k * kGatherThreads + threadIdx.x;
                 slot[k] = kNoRow;
-                code[k] = make_uint2(0, 0);
+                code[k] = make_uint4(0, 0, 0, 0);
                 scale[k] = 127;
                 if (j < n) {
                     const int r = (int)__umulhi((uint32_t)j, p.row_magic), c = j - r * p.per_row;
                     slot[k] = s_slot[buf][r];
                     if (slot[k] >= 0) {
                         const int blk = slot[k] >> p.block_shift;
-                        code[k] = __ldcs(reinterpret_cast<const uint2*>(p.cache + (size_t)slot[k] * p.hkv * D) + c);
+                        code[k] = __ldcs(reinterpret_cast<const uint4*>(p.cache + (size_t)slot[k] * p.hkv * D) + c);
                         scale[k] = __ldg(p.scales + ((size_t)blk * p.hkv + c / CPH) * p.block_size +
                                          (slot[k] & (p.block_size - 1)));
                     }
@@ -192,19 +201,18 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Gather
 #pragma unroll
             for (int k = 0; k < kGatherPer; ++k) {
                 if (slot[k] == kNoRow) continue;
-                const float f = scale_value(scale[k]);
-                const uint32_t in[2] = {code[k].x, code[k].y};
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t a, b;
-                    e4m3x4_to_half2(in[i], a, b);
-                    const float2 x = __half22float2(*reinterpret_cast<__half2*>(&a));
-                    const float2 y = __half22float2(*reinterpret_cast<__half2*>(&b));
-                    w[2 * i] = pack_bf16x2(x.x * f, x.y * f);
-                    w[2 * i + 1] = pack_bf16x2(y.x * f, y.y * f);
+                const RowScale f = row_scale(scale[k]);
+                uint4 w[2];
+                if (f.half != 0) widen16(code[k], f.half, w[0], w[1]);
+                else widen16_any(code[k], f.value, w[0], w[1]);
+                uint4* to = dst + 2 * (base + k * kGatherThreads + threadIdx.x);
+                if (p.dst_v8) {
+                    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+                    st_global_v8(to, v);
+                } else {
+                    to[0] = w[0];
+                    to[1] = w[1];
                 }
-                dst[base + k * kGatherThreads + threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
         if (row0 >= p.total_k - step) break;   // (row0 + step may pass 2^31)
@@ -267,7 +275,8 @@ nvpa_status_t run_gather_kv_fp8(void* dst, const void* cache, const uint8_t* sca
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     p.block_shift = __builtin_ctz((unsigned)block_size);
-    p.per_row = hkv * (head_dim / 8);
+    p.per_row = hkv * (head_dim / 16);
+    p.dst_v8 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
     p.tile_rows = std::max(1, kGatherChunks / p.per_row);
     p.row_magic = (uint32_t)(((1ull << 32) + p.per_row - 1) / p.per_row);
     p.err = err_flag;

@@ -100,14 +100,6 @@ __device__ __forceinline__ float exp_row(const uint32_t (&sv)[N], uint32_t p_col
     return (a0 + b0) + (a1 + b1);
 }
 
-// One 32-byte global store (the address must be 32-byte aligned).
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
-                    "r"(w[7])
-                 : "memory");
-}
-
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
