@@ -198,6 +198,7 @@ DECODE_SOURCES = ["paged_kv_cache_422_b200/csrc/paged_attention.cu",
 
 # sources of the tcgen05 attention kernel, the dominant kernel of a prefill step
 PREFILL_SOURCES = ["paged_kv_cache_422_b200/csrc/prefill_tcgen05.cu",
+                   "paged_kv_cache_422_b200/csrc/tile_softmax.cuh",
                    "paged_kv_cache_422_b200/csrc/sm100.cuh",
                    "paged_kv_cache_422_b200/csrc/attn_warp.cuh",
                    "paged_kv_cache_422_b200/csrc/common.cuh"]
