@@ -1014,7 +1014,8 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     p.scale_log2 = c.scale * kLog2e;
     cudaError_t e = cudaSuccess;
     if (p.planned) {
-        row_plan_kernel<<<1, 1024, 0, stream>>>(p);
+        // (its time is barriers and load latency: fewer warps where they suffice, 0.4 us)
+        row_plan_kernel<<<1, (long long)c.batch * r.row_tiles <= 256 ? 256 : 1024, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_failure(e, "row attention plan launch");
         count_launches(1);
