@@ -65,7 +65,7 @@ namespace {
 
 constexpr int kRows = 128;        // query rows per tile (MMA M)
 constexpr int kKeys = 128;        // keys per tile
-constexpr int kProducers = 3;     // warps that issue copies: 0, 2 and 3
+constexpr int kProducers = 3;     // warps that may issue copies: 0, 2 and 3
 constexpr int kUnits = 4;         // claimed units handed from the producer to the others
 constexpr int kBuckets = 4096;    // plan: key-tile counts sorted exactly
 constexpr int kGran = 16;         // granularity of the virtual key range
@@ -78,7 +78,7 @@ struct Roles {
     static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
     static constexpr int SMALL_REGS = FP8 ? 80 : 104;      // warps 0..3 and 12..15
     static constexpr int SOFTMAX_REGS = FP8 ? 176 : 200;   // warps 4..11
-    static constexpr int READERS = 1 + 2 + 8 + (FP8 ? 4 : 0);  // of the unit ring
+    static constexpr int READERS = 1 + 8 + (FP8 ? 4 : 0);  // of the unit ring, and producers but the first
     // shared memory at head_dim 128: Q tiles and K/V tiles (bf16, ready for the MMAs) of 32 KB,
     // staged e4m3 tiles of 16 KB.  A tile takes 2 us from its copy's issue to its arrival, so
     // the e4m3 cache's copies run four tiles ahead of the widening.
@@ -348,6 +348,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
     ChunkUnit* unit_ring = reinterpret_cast<ChunkUnit*>(smem + L::UNIT_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int producers = min(kProducers, kKeys / p.piece);   // at most one per piece of a tile
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -362,17 +363,17 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             mbar_init(bars + L::B_QEMPTY + q, 1);
         }
         for (int s = 0; s < R::RING; ++s) {
-            mbar_init(bars + L::B_KVFULL + s, FP8 ? 4 : kProducers);
+            mbar_init(bars + L::B_KVFULL + s, FP8 ? 4 : producers);
             mbar_init(bars + L::B_KVEMPTY + s, 1);
         }
         for (int s = 0; s < R::STAGES; ++s) {
-            mbar_init(bars + L::B_STFULL + s, kProducers);
+            mbar_init(bars + L::B_STFULL + s, producers);
             mbar_init(bars + L::B_STEMPTY + s, 4);
         }
         mbar_init(bars + L::B_DRAIN, 1);
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(bars + L::B_UFULL + i, 1);
-            mbar_init(bars + L::B_UEMPTY + i, R::READERS);
+            mbar_init(bars + L::B_UEMPTY + i, R::READERS + producers - 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -409,13 +410,13 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
 
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::SMALL_REGS));
-      if (warp != 1) {
+      if (warp == 0 || (warp >= 2 && warp - 1 < producers)) {
         // ============================ producers ============================
-        // Three warps copy every tile together, a third of its pieces each: with 16-row pieces
+        // Up to three warps copy every tile together, a share of its pieces each: with 16-row pieces
         // one issuing thread needs 200 cycles per piece and 64 columns, 6600 for the 32 of a K
         // and V tile, where the MMAs and softmaxes of a pair need half of that.
         const int pw = warp == 0 ? 0 : warp - 1;
-        const int pc = pw + kProducers * lane;     // this lane's piece of every tile
+        const int pc = pw + producers * lane;      // this lane's piece of every tile
         uint32_t fill = 0, qfill = 0;
         constexpr int kNoPiece = INT_MIN;
         const int piece = p.piece;
@@ -517,7 +518,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 uint8_t* tile = smem + (FP8 ? L::STAGE_OFF + slot * L::STAGE_BYTES : L::RING_OFF + slot * L::TILE_BYTES);
                 if constexpr (!FP8) {
                     for (uint32_t m = __ballot_sync(0xffffffffu, bad); m != 0; m &= m - 1) {
-                        const int c = pw + kProducers * (__ffs(m) - 1);
+                        const int c = pw + producers * (__ffs(m) - 1);
                         for (int r = 0; r < L::REGIONS; ++r) {
                             uint4* rows = reinterpret_cast<uint4*>(tile + r * L::REGION_BYTES + c * piece * 128);
                             for (int k = lane; k < piece * 8; k += 32) rows[k] = make_uint4(0, 0, 0, 0);
@@ -580,7 +581,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             drain(bars + (FP8 ? L::B_STFULL : L::B_KVFULL), fill, FP8 ? R::STAGES : R::RING);
             drain(bars + L::B_QFULL, qfill, QBUFS);
         }
-      } else {
+      } else if (warp == 1) {
         // ============================ MMA issuer ============================
         const uint32_t IDESC_QK = idesc_bf16_f32(kRows, kKeys, false) | (p.negate_qk ? (1u << 13) : 0u);
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(kRows, D, true);
@@ -617,10 +618,10 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             if (__shfl_sync(0xffffffffu, u.seq, 0) < 0) break;
             const int nk[2] = {__shfl_sync(0xffffffffu, u.nk[0], 0), __shfl_sync(0xffffffffu, u.nk[1], 0)};
             const int nkv = max(nk[0], nk[1]);
-            // the S after which Q_x is not read again (split: A and B share one Q)
-            auto last_q = [&](int x, int j) {
-                return p.split ? j == nk[0] - 1 && x == (nk[1] == nk[0] ? 1 : 0) : j == nk[x] - 1;
-            };
+            // the key tile after whose S tile x's Q buffer is free (split: A and B share one Q, which
+            // the later of their last S's releases)
+            const bool b_last = nk[1] == nk[0];
+            const int q_free[2] = {p.split && b_last ? -1 : nk[0] - 1, p.split ? (b_last ? nk[0] - 1 : -1) : nk[1] - 1};
             // S of key tile 0: tile A as soon as Q_A and K_0 are in, then tile B
             uint32_t qsl[2] = {0, 0};
             bool have = false;
@@ -645,7 +646,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 const bool done = p.split || x == 1 || nk[1] == 0;   // with this K tile
                 if (lane == 0) {
                     issue_qk(x, f % R::RING, qsl[x]);
-                    if (last_q(x, 0)) umma_commit(bars + L::B_QEMPTY + qsl[x]);
+                    if (q_free[x] == 0) umma_commit(bars + L::B_QEMPTY + qsl[x]);
                     if (done) umma_commit(bars + L::B_KVEMPTY + f % R::RING);
                 }
                 __syncwarp();
@@ -692,7 +693,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                         }
                         if (lane == 0) {
                             issue_qk(x, fk % R::RING, qsl[x]);
-                            if (last_q(x, j + 1)) umma_commit(bars + L::B_QEMPTY + qsl[x]);
+                            if (j + 1 == q_free[x]) umma_commit(bars + L::B_QEMPTY + qsl[x]);
                         }
                         __syncwarp();
                     }
@@ -761,6 +762,10 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const int a_min = __reduce_min_sync(0xffffffffu, va);
             const int b_max = __reduce_max_sync(0xffffffffu, vb);
             const int c_min = __reduce_min_sync(0xffffffffu, vc);
+            // key tiles without a mask anywhere in the warp: [open_lo, open_hi), and the whole tiles
+            // of long sinks, [0, open_sinks)
+            const int open_lo = max(0, (b_max - v0 + kKeys - 1) / kKeys), open_hi = (c_min - v0) / kKeys;
+            const int open_sinks = (a_min - v0) / kKeys;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < nk; ++j) {
@@ -770,16 +775,14 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 }
                 ++s_use;
                 tc_fence_after();
-                const int base = v0 + j * kKeys;
+                const bool open = (j >= open_lo && j < open_hi) || j < open_sinks;
                 if (!idle) {
-                    // no mask anywhere in the warp
-                    const bool open = base + kKeys <= c_min && (base >= b_max || base + kKeys <= a_min);
                     uint32_t sv[kKeys];
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c)
                         tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
                     tmem_wait_ld();
-                    if (!open) mask_columns(sv, base, va, vb, vc);
+                    if (!open) mask_columns(sv, v0 + j * kKeys, va, vb, vc);
                     const float mt = row_max<kKeys>(sv) * p.scale_log2;
                     const bool over = mt > m + kRescaleSlack;
                     const bool rescale = __any_sync(0xffffffffu, over);
@@ -816,7 +819,9 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     // V rows that nobody in the pair sees hold stale values, or what the ring
                     // held before: zeroed here, a row per thread, by the warps of the first tile
                     // whose P V reads them (the widening does it for the e4m3 cache)
-                    if ((base + kKeys > pc || (base < pb && base + kKeys > pa)) && (p.split || x == 0 || j >= u.nk[0])) {
+                    const int base = v0 + j * kKeys;
+                    if (!open && (base + kKeys > pc || (base < pb && base + kKeys > pa)) &&
+                        (p.split || x == 0 || j >= u.nk[0])) {
                         // ring position of V_j: behind the K_0s and 2 j tiles of this stream, and
                         // what the other stream has passed
                         const int sn1 = u.sn[1];
@@ -903,7 +908,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::SMALL_REGS));
         if constexpr (FP8) {
             const int r = (warp - 12) * 32 + lane;    // key row of the tile
-            const int prow = r / p.piece;             // its piece, copied by producer prow % 3
+            const int prow = r / p.piece;             // its piece: number prow / producers of a producer
+            const int of = prow % producers, bit = prow / producers;
             uint32_t fill = 0;
             bool ok = true;
             for (int n = 0; ok; ++n) {
@@ -920,7 +926,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     }
                     // rows that nobody in the pair sees, or whose block id is bad, become zero
                     const int key = keys.real(u.first_key(p, w.x) + w.j * kKeys + r);
-                    const uint32_t present = stage_mask[slot * kProducers + prow % kProducers] >> (prow / kProducers);
+                    const uint32_t present = stage_mask[slot * kProducers + of] >> bit;
                     const bool seen = (present & 1) && key <= keys.p_last &&
                                       (p.window == 0 || key > keys.p_first - p.window || key < p.sinks);
                     const RowScale f = row_scale(smem[L::SCALE_OFF + slot * kKeys + r]);
