@@ -228,3 +228,55 @@ def test_refusals_of_memory_elsewhere(cuda_device):
         _chunk(case, t, workspace=torch.empty(need - 256, dtype=torch.uint8, device=dev))
     with pytest.raises(nvpa.NvpaError):
         _chunk(case, t, max_ctx=(1 << 30) + 1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_blocks_behind_four_gigabytes(cuda_device, fp8):
+    """The same rows in the last blocks of a pool of more than 2^32 bytes and in a small pool:
+    equal bits from every call."""
+    dev = cuda_device
+    hkv, d, bs, used = 8, 128, 256, 5
+    row = hkv * d * (1 if fp8 else 2)
+    nb = (1 << 32) // (bs * row) + 7
+    case = Case(17, [700, 513], [40, 300], 16, hkv, d, bs, fp8, window=600, sinks=4)
+    t = case.device(dev)
+    assert case.num_blocks >= used
+    shift = nb - case.num_blocks
+    big = dict(t, tables=torch.where((t["tables"] >= 0) & (t["tables"] < case.num_blocks), t["tables"] + shift, t["tables"]))
+    for x in "kv":
+        small = t[x + "_cache"]
+        pool = torch.empty((nb,) + small.shape[1:], dtype=small.dtype, device=dev)
+        pool.view(torch.uint8)[shift:] = small.view(torch.uint8)
+        big[x + "_cache"] = pool
+        if fp8:
+            sc = torch.empty((nb,) + t[x + "_scales"].shape[1:], dtype=torch.uint8, device=dev)
+            sc[shift:] = t[x + "_scales"]
+            big[x + "_scales"] = sc
+    a, la = _chunk(case, t)
+    check_answers(case, a, la, TILE_BITS, "small pool")
+    b, lb = _chunk(case, big)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    # the row kernel: one token per sequence, and two
+    for news in ([1, 1], [2, 2]):
+        cu = torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device=dev)
+        q = t["q"][:sum(news)].contiguous()
+        got = []
+        for p in (t, big):
+            args = (q, p["k_cache"], p["v_cache"], p["tables"])
+            kw = dict(window=600, num_sinks=4, k_scales=p["k_scales"], v_scales=p["v_scales"], return_lse=True)
+            got.append(nvpa.chunk_attention(*args, cu, t["lens"], news[0], 700, case.scale, **kw) if news[0] > 1 else
+                       nvpa.paged_decode_attention_window(*args, t["lens"], 700, case.scale, **kw))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    if fp8:
+        # new rows into the last slots, and read back
+        g = torch.Generator(device=dev).manual_seed(1)
+        k = torch.randn((300, hkv, d), generator=g, device=dev).to(torch.bfloat16)
+        slots = torch.arange(nb * bs - 300, nb * bs, dtype=torch.int32, device=dev)
+        nvpa.store_kvcache_fp8(k, k, big["k_cache"], big["v_cache"], big["k_scales"], big["v_scales"], slots)
+        for x in "kv":
+            back = nvpa.gather_kv_fp8(big[x + "_cache"], big[x + "_scales"],
+                                      torch.tensor([[nb - 2, nb - 1]], dtype=torch.int32, device=dev),
+                                      torch.tensor([0, 512], dtype=torch.int32, device=dev), 512)[-300:]
+            # half a step of e4m3, 2^-4 relative, or half the smallest step of the row's scale
+            step = torch.exp2(big[x + "_scales"][-2:].double() - 127 - 10).transpose(1, 2).reshape(512, hkv)[-300:, :, None]
+            assert ((back.double() - k.double()).abs() <= torch.maximum(2.0 ** -4 * k.double().abs(), step)).all()
