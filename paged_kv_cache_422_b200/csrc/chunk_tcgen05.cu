@@ -897,7 +897,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 }
             }
             if (row_ok) {
-                if (partial) __stcg(p.lse_part + prow, lse);
+                if (partial) __stcg(p.lse_part + prow, lse == lse ? lse : INFINITY);   // (NaN: as in the row kernel)
                 else if (p.lse_out != nullptr) p.lse_out[orow] = lse;
             }
             pv_before += (uint32_t)nk;

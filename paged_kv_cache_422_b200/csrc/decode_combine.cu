@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4) decode_combine_kernel(c
     } else {
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
-    if (lane == 0 && p.lse_out != nullptr) p.lse_out[w] = tot > 0.f ? mx + __logf(tot) : -INFINITY;
+    // (a +inf among the lse, a partition whose scores are not numbers, makes tot and this NaN)
+    if (lane == 0 && p.lse_out != nullptr) p.lse_out[w] = tot == 0.f ? -INFINITY : mx + __logf(tot);
 }
 
 template <int D>

@@ -552,7 +552,9 @@ row_attention_kernel(const RowParams p) {
                 if constexpr (FP8) inv = sum == 0.f ? 0.f : inv * exp2f(mv[j][x] - m[j][x]);
                 const float lse = sum == 0.f ? -INFINITY : (m[j][x] + log2f(sum)) * kLn2;
                 if (g == 0) {
-                    if (ns > 1) __stcg(p.lse_part + row * p.s_max + s, lse);
+                    // (NaN as +inf: the combine drops a NaN from its maximum, and a row that
+                    // is not a number would come out as one without keys)
+                    if (ns > 1) __stcg(p.lse_part + row * p.s_max + s, lse == lse ? lse : INFINITY);
                     else if (p.lse_out != nullptr) p.lse_out[row] = lse;
                 }
                 if constexpr (FP8) {
