@@ -395,6 +395,17 @@ def _call(name, index, *args):
     check(st, name)
 
 
+def _c_ints(*sizes):
+    """The sizes as Python ints that fit a C int, so that none wraps around on its way in."""
+    sizes = [int(x) for x in sizes]
+    bits = 0
+    for x in sizes:
+        bits |= x
+    if bits >> 31 not in (0, -1):   # (a negative one, which may hide another here, is refused later)
+        raise ValueError(f"a size in {sizes} does not fit in 32 bits")
+    return sizes
+
+
 def _fp8_cache(cache, scales, cache_name="cache", scales_name="scales"):
     """(dimensions, device index) of one e4m3 pool [num_blocks, block_size, Hkv, D] with its
     scale bytes [num_blocks, Hkv, block_size]."""
@@ -497,9 +508,9 @@ def _workspace(workspace, like, index, stream, size, *args):
 
 def paged_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_context_len,
                                        block_size, window=0, num_sinks=0, num_splits=0) -> int:
-    return int(lib().nvpa_paged_decode_window_workspace_size(
-        batch, num_q_heads, num_kv_heads, head_dim, max_context_len, block_size, window, num_sinks,
-        num_splits))
+    return lib().nvpa_paged_decode_window_workspace_size(
+        batch, num_q_heads, num_kv_heads, head_dim, *_c_ints(
+            max_context_len, block_size, window, num_sinks, num_splits))
 
 
 def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_lens, max_context_len,
@@ -510,6 +521,8 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
     [B, Hq, D] bf16, one query per sequence, which sees the last `window` keys (0: all) and
     the first `num_sinks`."""
     (nb, bs, hkv, d), kind, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
+    max_context_len, window, num_sinks, num_splits = _c_ints(
+        max_context_len, window, num_sinks, num_splits)
     b, hq, out, lse = _window_outputs(q, d, index, stream, out, lse, return_lse)
     _expect(block_tables, _I32, "block_tables", 2, index)
     _expect(context_lens, _I32, "context_lens", (b,), index)
@@ -522,8 +535,8 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
         "nvpa_paged_decode_attention_window", index,
         out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind,
         _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), b, hq, hkv, d, nb, bs, int(max_context_len),
-        float(softmax_scale), int(window), int(num_sinks), int(num_splits), ws, ws_bytes,
+        context_lens.data_ptr(), b, hq, hkv, d, nb, bs, max_context_len, float(softmax_scale),
+        window, num_sinks, num_splits, ws, ws_bytes,
         _flag_ptr(err_flag, index), _raw_stream(index, stream))
     return (out, lse) if return_lse else out
 
@@ -531,9 +544,9 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
 def chunk_attention_workspace_size(batch, total_q, num_q_heads, num_kv_heads, head_dim,
                                    max_seqlen_q, max_context_len, block_size, window=0,
                                    num_sinks=0, num_splits=0) -> int:
-    return int(lib().nvpa_chunk_attention_workspace_size(
-        batch, total_q, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_context_len,
-        block_size, window, num_sinks, num_splits))
+    return lib().nvpa_chunk_attention_workspace_size(
+        batch, total_q, num_q_heads, num_kv_heads, head_dim, *_c_ints(
+            max_seqlen_q, max_context_len, block_size, window, num_sinks, num_splits))
 
 
 def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q,
@@ -545,6 +558,8 @@ def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_len
     ones included, in a bf16 cache, or an e4m3 one with its k_scales / v_scales; a query sees
     the last `window` keys up to its own (0: all) and the first `num_sinks`."""
     (nb, bs, hkv, d), kind, index = _any_cache(k_cache, v_cache, k_scales, v_scales)
+    max_seqlen_q, max_context_len, window, num_sinks, num_splits = _c_ints(
+        max_seqlen_q, max_context_len, window, num_sinks, num_splits)
     total_q, hq, out, lse = _window_outputs(q, d, index, stream, out, lse, return_lse)
     _expect(block_tables, _I32, "block_tables", 2, index)
     _expect(cu_seqlens_q, _I32, "cu_seqlens_q", 1, index)
@@ -559,8 +574,7 @@ def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_len
         "nvpa_chunk_attention", index,
         out.data_ptr(), _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind,
         _ptr(k_scales), _ptr(v_scales), block_tables.data_ptr(), block_tables.shape[1],
-        cu_seqlens_q.data_ptr(), context_lens.data_ptr(), batch, total_q, int(max_seqlen_q),
-        int(max_context_len), hq, hkv, d, nb, bs, float(softmax_scale), int(window),
-        int(num_sinks), int(num_splits), ws, ws_bytes, _flag_ptr(err_flag, index),
-        _raw_stream(index, stream))
+        cu_seqlens_q.data_ptr(), context_lens.data_ptr(), batch, total_q, max_seqlen_q,
+        max_context_len, hq, hkv, d, nb, bs, float(softmax_scale), window, num_sinks, num_splits,
+        ws, ws_bytes, _flag_ptr(err_flag, index), _raw_stream(index, stream))
     return (out, lse) if return_lse else out

@@ -138,6 +138,7 @@ struct GatherFp8Params {
     int dst_v8;            // dst is 32-byte aligned
     int tile_rows;
     uint32_t row_magic;    // ceil(2^32 / per_row): j / per_row = umulhi(j, row_magic) for j * per_row < 2^32
+                           // (tiles of one row: 0, whose quotient is always 0)
     int32_t* err;
 };
 
@@ -278,7 +279,7 @@ nvpa_status_t run_gather_kv_fp8(void* dst, const void* cache, const uint8_t* sca
     p.per_row = hkv * (head_dim / 16);
     p.dst_v8 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
     p.tile_rows = std::max(1, kGatherChunks / p.per_row);
-    p.row_magic = (uint32_t)(((1ull << 32) + p.per_row - 1) / p.per_row);
+    p.row_magic = p.tile_rows == 1 ? 0 : (uint32_t)(((1ull << 32) + p.per_row - 1) / p.per_row);
     p.err = err_flag;
     const long long tiles = ((long long)total_k + p.tile_rows - 1) / p.tile_rows;
     const int grid = (int)std::min<long long>(tiles, (long long)device_sm_count() * kGatherBlocks);

@@ -280,3 +280,20 @@ def test_blocks_behind_four_gigabytes(cuda_device, fp8):
             # half a step of e4m3, 2^-4 relative, or half the smallest step of the row's scale
             step = torch.exp2(big[x + "_scales"][-2:].double() - 127 - 10).transpose(1, 2).reshape(512, hkv)[-300:, :, None]
             assert ((back.double() - k.double()).abs() <= torch.maximum(2.0 ** -4 * k.double().abs(), step)).all()
+
+
+def test_sizes_that_do_not_fit_a_c_int_are_refused(cuda_device):
+    case = Case(36, [20, 20], [1, 1], 4, 2, 64, 16, True)
+    t = case.device(cuda_device)
+    pools = (t["q"], t["k_cache"], t["v_cache"], t["tables"])
+    sc = dict(k_scales=t["k_scales"], v_scales=t["v_scales"])
+    for big in (2 ** 31, 2 ** 32 + 20, 2 ** 40, -2 ** 33):
+        for name in ("window", "num_sinks", "num_splits"):
+            with pytest.raises(ValueError, match="32 bits"):
+                nvpa.paged_decode_attention_window(*pools, t["lens"], 20, 0.125, **sc, **{name: big})
+            with pytest.raises(ValueError, match="32 bits"):
+                nvpa.chunk_attention(*pools, t["cu"], t["lens"], 1, 20, 0.125, **sc, **{name: big})
+        with pytest.raises(ValueError, match="32 bits"):
+            nvpa.paged_decode_attention_window(*pools, t["lens"], big, 0.125, **sc)
+        with pytest.raises(ValueError, match="32 bits"):
+            nvpa.chunk_attention(*pools, t["cu"], t["lens"], big, 20, 0.125, **sc)

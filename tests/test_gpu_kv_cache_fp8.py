@@ -199,3 +199,15 @@ def test_gather_of_wide_rows_and_many_sequences(cuda_device, lens, hkv, d, bs):
     full = codes.view(torch.float8_e4m3fn).float() * torch.exp2(scales.float() - 127).transpose(1, 2)[..., None]
     want = torch.cat([full[tables[b, :need[b]].long()].flatten(0, 1)[:n] for b, n in enumerate(lens) if n])
     assert torch.equal(out.float(), want)      # a code times a power of two is a bf16 value
+
+
+def test_read_back_of_very_wide_rows(cuda_device):
+    # 66536 chunks of 16 codes in a row: more than 2^16
+    dev, hkv, d, bs, nb = cuda_device, 8317, 128, 16, 3
+    g = torch.Generator(device=dev).manual_seed(3)
+    codes = torch.randint(0, 127, (nb, bs, hkv, d), generator=g, device=dev, dtype=torch.uint8)
+    scales = torch.randint(100, 140, (nb, hkv, bs), generator=g, device=dev, dtype=torch.uint8)
+    tables = i32(np.array([[2, 0]]), dev)
+    out = nvpa.gather_kv_fp8(codes.view(torch.float8_e4m3fn), scales, tables, i32(np.array([0, 19]), dev), 19)
+    full = codes.view(torch.float8_e4m3fn).float() * torch.exp2(scales.float() - 127).transpose(1, 2)[..., None]
+    assert torch.equal(out.float(), torch.cat([full[2], full[0, :3]]))
