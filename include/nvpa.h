@@ -476,8 +476,9 @@ size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int n
  *                   aligned; calls that share a workspace must not overlap.
  *   max_context_len at most 2^30 (NVPA_ERR_UNSUPPORTED above).
  *   other arguments, out, lse and errors as for nvpa_paged_decode_attention.
- * The softmax weights are rounded to 16 significant bits (bf16 cache) or 11 (e4m3 cache)
- * before the product with the values; sums are float32.  A query with a visible score that is
+ * The softmax weights are rounded to 16 significant bits (bf16 cache) or 11 (e4m3 cache, and
+ * no finer than 2^-25 of the row's largest weight; the values' scales play no part) before the
+ * product with the values; sums are float32.  A query with a visible score that is
  * NaN gets NaN.  A sequence's result depends on its own
  * rows and on the call's host-side arguments only, not on the other sequences.
  */

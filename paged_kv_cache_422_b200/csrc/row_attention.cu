@@ -38,9 +38,15 @@
 // 1 in magnitude and rounded to fp16 (an error of 2^-25 of the row's largest element at
 // most: bf16 has 8 significant bits).  Weights are fp16 for the e4m3 cache (2^-11 relative)
 // and a sum of two bf16 (2^-17) for the bf16 cache, whose values are used as they are.
-// The fp16 weight includes the value's 2^e and is taken relative to the largest such weight
-// so far (a running maximum of its own beside the softmax's), so a scale of any size neither
-// overflows nor is lost beside larger ones.
+// The fp16 weight includes the value's 2^e and is taken relative to 2^-7 of the largest such
+// weight (a running maximum of its own beside the softmax's), so a scale of any size does not
+// overflow.  fp16 holds w = p 2^(e - gap) only to 2^-25 (p: the softmax weight relative to its
+// own reference, gap: the difference of the two references), which is 2^(gap - e - 25) of p: for
+// e >= gap at most 2^-25, as an fp16 softmax weight alone would have it, and 2^-32 where the
+// values' scales are alike.  A stage with a key of a smaller scale (rows 2^7 below the one that
+// counts most) takes float32 weights and CUDA-core products instead, which cost it about five
+// times as much.  (A second product for the weights below 2^-14 of every stage, with the values
+// scaled by 2^-15, costs 3 % of a decode and 17 to 26 % of the 16- and 24-row passes.)
 #include <algorithm>
 #include <cuda_fp16.h>
 #include <mutex>
@@ -53,6 +59,8 @@ namespace nvpa {
 namespace {
 
 constexpr int kRowWarps = 4;
+constexpr float kWeightTop = 7.f;   // log2 of the largest fp16 weight when its reference is set: with
+                                    // kRescaleSlack above it 2^15
 
 struct RowParams {
     const uint16_t* q;           // [total_q, hq, D]
@@ -267,7 +275,7 @@ struct RowStage {
 constexpr int kRowStages = 2;
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, D == 128 && FP8 && NT == 1 ? 3 : 0)
 row_attention_kernel(const RowParams p) {
     using Stage = RowStage<D, FP8, NT>;
     constexpr int STAGES = kRowStages;
@@ -472,6 +480,7 @@ row_attention_kernel(const RowParams p) {
     int pos[NT][2];                // their positions (-1: no such row)
     float o[NT][MT][4];
     float m[NT][2], mv[NT][2], l[NT][2];
+    float gap = 0.f;               // largest mv - m of this lane's rows
     uint32_t unset = 0;            // rows (bit 2 j + x) that have seen no key: their m and mv mean nothing yet
 
     auto start = [&](const int4& na, const int4& nb, int nhk) {
@@ -593,6 +602,51 @@ row_attention_kernel(const RowParams p) {
             }
     };
 
+    // Sums and O^T += V^T P^T of an e4m3 stage with float32 weights, key by key on the CUDA cores.
+    auto add_float32 = [&](const uint8_t* sb, const float (&sc)[TILES][NT][4], const float (&ew)[TILES][NT][4]) {
+        constexpr int N = D / 8;   // dims of this lane: g * N ..
+#pragma unroll
+        for (int u = 0; u < TILES; ++u)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                float w[NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        l[j][x] += fast_exp2(sc[u][j][2 * y + x]);
+                        w[j][x] = fast_exp2(ew[u][j][2 * y + x]);
+                    }
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {   // key k + 8 y of tile u, its weights from the lanes that have it
+                    float wk[NT][2];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) wk[j][x] = __shfl_sync(0xffffffffu, w[j][x], 4 * k + t);
+                    const uint8_t* vs = sb + u * 2 * Stage::KV + Stage::KV;
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2) {   // four dims
+                        const int dim = g * N + 2 * i;
+                        uint32_t h[2];
+                        e4m3x4_to_half2(*reinterpret_cast<const uint32_t*>(
+                            vs + Stage::at(k + 8 * y, dim >> 4) + (dim & 15)), h[0], h[1]);
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[z]));
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    o[j][i + z][x] = fmaf(wk[j][x], c.x, o[j][i + z][x]);
+                                    o[j][i + z][2 + x] = fmaf(wk[j][x], c.y, o[j][i + z][2 + x]);
+                                }
+                        }
+                    }
+                }
+            }
+    };
+
     auto consume = [&](int st, const int4& meta) {
         const uint8_t* sb = wsm + st * Stage::BYTES;
         const uint32_t sa = wbase + st * Stage::BYTES;
@@ -681,7 +735,7 @@ row_attention_kernel(const RowParams p) {
                     }
                 }
         };
-        float top = -INFINITY;
+        float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             arg(j);
@@ -702,12 +756,13 @@ row_attention_kernel(const RowParams p) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     top = fmaxf(top, sc[u][j][x]);
-                    if constexpr (FP8) top = fmaxf(top, ew[u][j][x]);
+                    if constexpr (FP8) topv = fmaxf(topv, ew[u][j][x]);
                 }
         }
         // lazy rescaling, as in attn_warp.cuh: the references move only when some exponent is
         // more than kRescaleSlack above them, and when a row sees its first keys
-        if (__any_sync(0xffffffffu, top > kRescaleSlack || unset != 0)) {
+        if (__any_sync(0xffffffffu, top > kRescaleSlack || topv > kWeightTop + kRescaleSlack || unset != 0)) {
+            gap = -INFINITY;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -719,7 +774,7 @@ row_attention_kernel(const RowParams p) {
                         if constexpr (FP8) upv = fmaxf(upv, fmaxf(ew[u][j][x], ew[u][j][2 + x]));
                     }
                     up = max_over_keys(up);
-                    upv = FP8 ? max_over_keys(upv) : up;
+                    upv = FP8 ? max_over_keys(upv) - kWeightTop : up;
                     const uint32_t bit = 1u << (2 * j + x);
                     const bool fresh = (unset & bit) != 0, some = up > -INFINITY;
                     if (!fresh) {
@@ -730,6 +785,7 @@ row_attention_kernel(const RowParams p) {
                     else unset &= ~bit;
                     m[j][x] += up;
                     mv[j][x] += upv;
+                    if (pos[j][x] >= 0 && !(unset & bit)) gap = fmaxf(gap, mv[j][x] - m[j][x]);
                     const float al = fresh ? 1.f : fast_exp2(-up), ao = fresh ? 1.f : fast_exp2(-upv);
                     l[j][x] *= al;
 #pragma unroll
@@ -748,6 +804,27 @@ row_attention_kernel(const RowParams p) {
         }
         uint32_t ph[TILES][NT][2], pl[TILES][NT][2];
         (void)pl;
+        if constexpr (FP8) {
+            // keys whose scale lies so far below the rows' that fp16 weights would lose them (see the top)
+            bool small = false;
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) small = small || fminf(ve[u][0], ve[u][1]) < gap;
+            if (__any_sync(0xffffffffu, small)) {
+                // (a key that no row sees, or whose weight is 0, does not count)
+                float most = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (ve[u][x >> 1] < gap) most = fmaxf(most, sc[u][j][x]);
+                if (__any_sync(0xffffffffu, most > -126.f)) {
+                    add_float32(sb, sc, ew);
+                    return;
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
