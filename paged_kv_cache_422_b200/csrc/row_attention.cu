@@ -34,9 +34,9 @@
 //   V fragment (A of O^T, dims x keys): bf16 through ldmatrix.trans; e4m3 by loading 16
 //     (D = 128) or 8 dims of the lane's four keys and interleaving pairs of keys with prmt.
 //   P^T (B of O^T): the scores lie with keys in rows; movmatrix transposes 8 x 8 tiles.
-// Rounding: an e4m3 code is exact in fp16; q is scaled by a power of two per row to at most
-// 1 in magnitude and rounded to fp16 (an error of 2^-25 of the row's largest element at
-// most: bf16 has 8 significant bits).  Weights are fp16 for the e4m3 cache (2^-11 relative)
+// Rounding: an e4m3 code is exact in fp16; q is scaled by a power of two per row to [2^14, 2^15)
+// for its largest element and rounded to fp16 (bf16 has 8 significant bits: exact for elements
+// down to 2^-31 of the largest, and off by 2^-39 of it at most).  Weights are fp16 for the e4m3 cache (2^-11 relative)
 // and a sum of two bf16 (2^-17) for the bf16 cache, whose values are used as they are.
 // The fp16 weight includes the value's 2^e and is taken relative to 2^-7 of the largest such
 // weight (a running maximum of its own beside the softmax's), so a scale of any size does not
@@ -512,10 +512,12 @@ row_attention_kernel(const RowParams p) {
                 mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
                 for (int x = 1; x < 4; x <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-                // 2^-eq brings the row into (-2, 2); rows too small or not finite stay in range
-                const int eq = min(max((int)(mx >> 7), 1), 253);
-                const float inv = scale_value(254 - eq);
-                fac *= scale_value(eq);
+                // the largest element to [2^14, 2^15), near the top of fp16's range (a largest one of
+                // 2^127 or more to 2^15 at most times 1.9922, still below 65504); rows too small or
+                // not finite stay in range
+                const int eq = min(max((int)(mx >> 7), 15), 253);
+                const float inv = scale_value(254 + 14 - eq);
+                fac *= scale_value(eq - 14);
 #pragma unroll
                 for (int i = 0; i < KK; ++i)
                     set_q(j, i, pack_half2(bf16_lo(w[i][0]) * inv, bf16_hi(w[i][0]) * inv),

@@ -1,10 +1,11 @@
-"""Values far apart: what a small weight or a small row adds shows in the channels that nothing
-larger reaches, wherever its key lies."""
+"""Values far apart: what a small weight, a small query element or a small row adds shows in the
+channels that nothing larger reaches, wherever its key lies."""
 
 import numpy as np
 import pytest
 
 import paged_kv_cache_422_b200 as nvpa
+from oracle.paged_attention import bf16_to_f64
 from oracle.window_attention import dequantise_rows, gather, quantise_rows
 from synth.workloads import bf16_bits_from_f32
 from tests.window_helpers import ROW_BITS, TILE_BITS, Case, check_answers
@@ -92,5 +93,41 @@ def test_many_small_weights_beside_a_large_one(cuda_device, new, first):
     set_rows(case, 0, k)
     set_rows(case, 1, v)
     for num_splits in (0, 1, 3):
+        out, lse = run(case, cuda_device, num_splits)
+        check_answers(case, out, lse, bits_of(case), f"{num_splits} splits")
+
+
+class FineQuery(Case):
+    """The share of the query's rounding in the bounds at 2^-39 of its largest element (top
+    elements are scaled to [2^14, 2^16) and fp16 steps are 2^-24) instead of 2^-25."""
+
+    def answers(self):
+        out, lse, ob, mass, lb = super().answers()
+        q = bf16_to_f64(self.q)
+        for b, (n, m) in enumerate(zip(self.lens, self.news)):
+            rows = slice(self.cu[b], self.cu[b + 1])
+            kabs = np.abs(gather(self.values[0], self.tables[b], n, self.bs)).sum(-1).max(0)
+            share = 2.0 ** -25 * abs(self.scale) * np.abs(q[rows]).max(-1) * \
+                np.repeat(kabs, self.hq // self.hkv)[None, :]
+            ob[rows] -= (2 * share * (1 - 2.0 ** -14))[..., None] * mass[rows]
+            lb[rows] -= share * (1 - 2.0 ** -14)
+        return out, lse, ob, mass, lb
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", NEWS)
+@pytest.mark.parametrize("gap", [12, 20, 26])
+def test_query_elements_of_very_different_size(cuda_device, d, new, gap):
+    """A query's largest element meets keys that are zero there; the scores come from elements
+    2^-gap of it."""
+    case = FineQuery(71 + d, [150, 40], [new, 1], 4, 1, d, 16, True, scale=1.0)
+    rng = np.random.default_rng(gap)
+    q = (rng.standard_normal(case.q.shape) * 2.0 ** -gap).astype(np.float32)
+    q[..., 3] = 1.5
+    case.q = bf16_bits_from_f32(q).reshape(q.shape)
+    k = rng.standard_normal(case.kv_bits[0].shape) * 2.0 ** (gap - 3)
+    k[..., 3] = 0
+    set_rows(case, 0, k)
+    for num_splits in (0, 2):
         out, lse = run(case, cuda_device, num_splits)
         check_answers(case, out, lse, bits_of(case), f"{num_splits} splits")
