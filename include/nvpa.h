@@ -479,9 +479,10 @@ size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int n
  * The softmax weights are rounded to 16 significant bits (bf16 cache) or 11 (e4m3 cache, and
  * no finer than 2^-25 of the row's largest weight; the values' scales play no part) before the
  * product with the values; the e4m3 cache's queries are held to 2^-39 of the row's largest
- * element; sums are float32.  A query with a visible score that is NaN gets NaN.  A sequence's
- * result depends on its own rows and on the call's host-side arguments only, not on the other
- * sequences.
+ * element; sums are float32.  A query with a visible score that is NaN gets NaN; an infinite value
+ * (bf16 cache) with a weight of at least 2^-100 of the row's largest makes its dim infinite, or NaN
+ * beside one of the other sign.  A sequence's result depends on its own rows and on the call's
+ * host-side arguments only, not on the other sequences.
  */
 nvpa_status_t nvpa_paged_decode_attention_window(
     void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,

@@ -37,7 +37,8 @@
 // Rounding: an e4m3 code is exact in fp16; q is scaled by a power of two per row to [2^14, 2^15)
 // for its largest element and rounded to fp16 (bf16 has 8 significant bits: exact for elements
 // down to 2^-31 of the largest, and off by 2^-39 of it at most).  Weights are fp16 for the e4m3 cache (2^-11 relative)
-// and a sum of two bf16 (2^-17) for the bf16 cache, whose values are used as they are.
+// and a sum of two bf16 for the bf16 cache, whose values are used as they are: its upper half cut
+// off (2^-7) and the rest rounded (2^-9 of it), 2^-16 in all.
 // The fp16 weight includes the value's 2^e and is taken relative to 2^-7 of the largest such
 // weight (a running maximum of its own beside the softmax's), so a scale of any size does not
 // overflow.  fp16 holds w = p 2^(e - gap) only to 2^-25 (p: the softmax weight relative to its
@@ -844,9 +845,13 @@ row_attention_kernel(const RowParams p) {
                 } else {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const uint32_t h = pack_bf16x2(w[2 * y], w[2 * y + 1]);
+                        // the upper halves, and what is left plus 2^-24 of them: never 0 or of the other
+                        // sign beside a weight, so that an infinite value stays one
+                        constexpr float kRest = 1.f - 0x1p-24f;
+                        const uint32_t h = __byte_perm(__float_as_uint(w[2 * y]), __float_as_uint(w[2 * y + 1]), 0x7632);
                         ph[u][j][y] = transpose8x8(h);
-                        pl[u][j][y] = transpose8x8(pack_bf16x2(w[2 * y] - bf16_lo(h), w[2 * y + 1] - bf16_hi(h)));
+                        pl[u][j][y] = transpose8x8(pack_bf16x2(fmaf(-bf16_lo(h), kRest, w[2 * y]),
+                                                               fmaf(-bf16_hi(h), kRest, w[2 * y + 1])));
                     }
                 }
             }
