@@ -48,7 +48,6 @@
 // drain take 5 us (e4m3 8).
 #include <algorithm>
 #include <cfloat>
-#include <climits>
 #include <cmath>
 #include <mutex>
 
@@ -418,7 +417,6 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         const int pw = warp == 0 ? 0 : warp - 1;
         const int pc = pw + producers * lane;      // this lane's piece of every tile
         uint32_t fill = 0, qfill = 0;
-        constexpr int kNoPiece = INT_MIN;
         const int piece = p.piece;
         const bool has_piece = pc * piece < kKeys;
         // Warp 0 claims units, one ahead of the one whose copies are issued.
@@ -472,12 +470,14 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const int va0 = cur.first_key(p, 0) + pc * piece, vb0 = cur.first_key(p, 1) + pc * piece;
             const int vend = keys.upto(keys.p_last);        // virtual keys of the unit's rows
             const int32_t* bt = p.block_tables + (size_t)cur.seq * p.max_blocks;
-            // The block id of this lane's piece of key tile j of stream x (range-checked where it
-            // is used); pieces past the last visible key are not looked up.
+            // The first key of this lane's piece of key tile j of stream x, whether there is one (pieces
+            // past the last visible key are not looked up), and its block id (range-checked where it is
+            // used).
+            auto piece_key = [&](int x, int j) { return (x ? vb0 : va0) + j * kKeys; };
+            auto is_piece = [&](int v) { return has_piece && v < vend; };
             auto load_piece = [&](int x, int j) {
-                const int v = (x ? vb0 : va0) + j * kKeys;
-                return has_piece && j < (x ? sn1 : sn0) && v < vend ? __ldg(bt + (keys.real(v) >> p.block_shift))
-                                                                    : kNoPiece;
+                const int v = piece_key(x, j);
+                return j < (x ? sn1 : sn0) && is_piece(v) ? __ldg(bt + (keys.real(v) >> p.block_shift)) : -1;
             };
             // of each stream's current key tile and the next
             int blk_a = load_piece(0, 0), next_a = load_piece(0, 1);
@@ -511,8 +511,9 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                                abort_flag, p.err))
                     return false;
                 ++fill;
-                const bool in_range = blk >= 0 && blk < p.num_blocks;
-                const bool bad = blk != kNoPiece && !in_range;
+                const int v = piece_key(x, j);
+                const bool good = blk >= 0 && blk < p.num_blocks;
+                const bool in_range = is_piece(v) && good, bad = is_piece(v) && !good;
                 if (kv == 0 && bad) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
                 const uint32_t valid = __ballot_sync(0xffffffffu, in_range);
                 uint8_t* tile = smem + (FP8 ? L::STAGE_OFF + slot * L::STAGE_BYTES : L::RING_OFF + slot * L::TILE_BYTES);
@@ -535,7 +536,7 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 __syncwarp();
                 if (in_range) {
                     const CUtensorMap* map = kv ? &v_map : &k_map;
-                    const int row = keys.real((x ? vb0 : va0) + j * kKeys) & (p.block_size - 1);
+                    const int row = keys.real(v) & (p.block_size - 1);
                     const int z = blk * p.block_size + row;
                     if constexpr (FP8) {
                         tma_load_3d(tile + pc * piece * D, map, full, 0, cur.hk, z);
