@@ -27,7 +27,8 @@
 // few rows of one tile instead of a tile of their own.  With a window, tiles are copied in
 // pieces of 16 rows (a tile may start anywhere); without, in pieces of min(block, 128) rows.
 // Rows that nobody in the unit sees are masked by -inf scores and zeroed values (never by
-// arithmetic that would keep a NaN), and blocks without a visible key are not looked up.
+// arithmetic that would keep a NaN), and so are those of blocks whose ids are out of range; blocks
+// without a visible key are not looked up.
 //
 // Warp roles (one persistent CTA per SM, units claimed longest first):
 //   warps 0 2 3  copy Q and K/V tiles by TMA (e4m3: codes and scales into a staging ring);
@@ -68,6 +69,8 @@ constexpr int kProducers = 3;     // warps that may issue copies: 0, 2 and 3
 constexpr int kUnits = 4;         // claimed units handed from the producer to the others
 constexpr int kBuckets = 4096;    // plan: key-tile counts sorted exactly
 constexpr int kGran = 16;         // granularity of the virtual key range
+constexpr int kKeeps = 8;         // K tiles whose masks of present keys are held: the copies run at most 4
+                                  // ahead of the softmax (half of the slots of the rings)
 
 // Registers per thread after setmaxnreg: the shares of the warpgroups add up to the launch's.
 template <bool FP8>
@@ -210,9 +213,10 @@ struct ChunkLayout {
     static constexpr int B_UFULL = B_DRAIN + 1, B_UEMPTY = B_UFULL + kUnits;
     static constexpr int B_STFULL = B_UEMPTY + kUnits, B_STEMPTY = B_STFULL + R::STAGES;
     static constexpr int NBARS = B_STEMPTY + R::STAGES;
-    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;     // tmem base, abort flag, staged piece masks
-    static constexpr int UNIT_OFF = (MISC_OFF + 8 + 4 * kProducers * R::STAGES + 15) / 16 * 16;
-    static constexpr int BYTES = UNIT_OFF + (int)sizeof(ChunkUnit) * kUnits;
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;     // tmem base, abort flag, bad block seen, staged piece masks
+    static constexpr int UNIT_OFF = (MISC_OFF + 12 + 4 * kProducers * R::STAGES + 15) / 16 * 16;
+    static constexpr int KEEP_OFF = UNIT_OFF + (int)sizeof(ChunkUnit) * kUnits;
+    static constexpr int BYTES = KEEP_OFF + kKeeps * (kKeys / 8);
     static constexpr int ALLOC = BYTES + 1024;               // room to align the base to 1024
 };
 static_assert(ChunkLayout<128, false>::ALLOC <= 227 * 1024 && ChunkLayout<128, true>::ALLOC <= 227 * 1024,
@@ -316,12 +320,13 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const ChunkParams p) {
 // ------------------------------------------------------------------------------------
 
 // Columns of S (virtual keys base ..) that a row does not see become -inf; it sees virtual
-// keys [0, a) and [b, c).
-__device__ __forceinline__ void mask_columns(uint32_t (&sv)[kKeys], int base, int a, int b, int c) {
+// keys [0, a) and [b, c) but those without a bit in `keep`.
+__device__ __forceinline__ void mask_columns(uint32_t (&sv)[kKeys], int base, int a, int b, int c,
+                                             const volatile uint32_t* keep) {
 #pragma unroll
     for (int i = 0; i < kKeys / 32; ++i) {
         const int at = base + 32 * i;
-        const uint32_t vm = (visible_mask(a - at) | ~visible_mask(b - at)) & visible_mask(c - at);
+        const uint32_t vm = (visible_mask(a - at) | ~visible_mask(b - at)) & visible_mask(c - at) & keep[i];
 #pragma unroll
         for (int k = 0; k < 32; ++k)
             sv[i * 32 + k] = __float_as_uint(keep_or(sv[i * 32 + k], vm, k, -INFINITY));
@@ -343,8 +348,12 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
-    uint32_t* stage_mask = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF + 8);   // [stage][producer] its pieces present
+    volatile int* bad_seen = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 8);   // a block id out of range so far
+    uint32_t* stage_mask = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF + 12);   // [stage][producer] its pieces present
     ChunkUnit* unit_ring = reinterpret_cast<ChunkUnit*>(smem + L::UNIT_OFF);
+    // [K tile, modulo kKeeps] a bit per key: 0 where its block id is out of range
+    volatile uint32_t* keeps = reinterpret_cast<volatile uint32_t*>(smem + L::KEEP_OFF);
+    constexpr int KEEP = kKeys / 32;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int producers = min(kProducers, kKeys / p.piece);   // at most one per piece of a tile
@@ -375,11 +384,13 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             mbar_init(bars + L::B_UEMPTY + i, R::READERS + producers - 1);
         }
         *abort_flag = 0;
+        *bad_seen = 0;
         fence_mbar_init();
         tma_prefetch_desc(&q_map);
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
     }
+    if (threadIdx.x < kKeeps * KEEP) keeps[threadIdx.x] = 0xffffffffu;
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -417,6 +428,8 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         const int pw = warp == 0 ? 0 : warp - 1;
         const int pc = pw + producers * lane;      // this lane's piece of every tile
         uint32_t fill = 0, qfill = 0;
+        uint32_t kfill = 0;                        // K tiles so far
+        bool was_bad = false;                      // this lane has met a block id out of range
         const int piece = p.piece;
         const bool has_piece = pc * piece < kKeys;
         // Warp 0 claims units, one ahead of the one whose copies are issued.
@@ -502,7 +515,9 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 return true;
             };
             // This warp's share of K (kv = 0) or V of key tile j.  A block id out of range is
-            // flagged (once, with K) and its rows are zero: their keys score 0 and add 0.
+            // flagged (once, with K), its rows are zero and its keys are absent: their bits in `keeps` are
+            // cleared ahead of K's arrival and so of S.  A lane writes the bits of its piece from the first
+            // such id that it meets on; nothing else clears them.
             auto load_kv = [&](int x, int kv, int j, int blk) -> bool {
                 constexpr int RING = FP8 ? R::STAGES : R::RING;
                 const int slot = fill % RING;
@@ -514,7 +529,18 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 const int v = piece_key(x, j);
                 const bool good = blk >= 0 && blk < p.num_blocks;
                 const bool in_range = is_piece(v) && good, bad = is_piece(v) && !good;
-                if (kv == 0 && bad) flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
+                was_bad = was_bad || bad;
+                if (kv == 0 && was_bad) {
+                    if (bad) {
+                        flag_error(p.err, NVPA_FLAG_BAD_BLOCK_ID);
+                        *bad_seen = 1;
+                    }
+                    volatile uint16_t* keep = reinterpret_cast<volatile uint16_t*>(
+                        keeps + kfill % kKeeps * KEEP) + pc * piece / 16;
+                    for (int i = 0; i < piece / 16; ++i) keep[i] = bad ? 0 : 0xffff;
+                    __threadfence_block();   // (lane 0 arrives below)
+                }
+                kfill += 1 - kv;
                 const uint32_t valid = __ballot_sync(0xffffffffu, in_range);
                 uint8_t* tile = smem + (FP8 ? L::STAGE_OFF + slot * L::STAGE_BYTES : L::RING_OFF + slot * L::TILE_BYTES);
                 if constexpr (!FP8) {
@@ -767,6 +793,10 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             // of long sinks, [0, open_sinks)
             const int open_lo = max(0, (b_max - v0 + kKeys - 1) / kKeys), open_hi = (c_min - v0) / kKeys;
             const int open_sinks = (a_min - v0) / kKeys;
+            // which of the unit's K tiles is key tile j of this tile's stream, in the order of the walk: K_0, K_1,
+            // ... or, split, A's K_0, B's K_0, A's K_1, ... until B has no more
+            const int sn1 = u.sn[1];
+            auto k_order = [&](int j) { return p.split && x ? 2 * j + 1 : j + min(j, sn1); };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < nk; ++j) {
@@ -782,8 +812,13 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c)
                         tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+                    // (behind S, and so behind K's arrival.  Masks in shared memory that are all ones but for
+                    // bad blocks: whole prompts 267 -> 271 us, 512-token chunks as before; looking the
+                    // blocks up here, in line or in a function, costs calls without any 2 to 5 %.)
+                    const bool bad = *bad_seen != 0;
                     tmem_wait_ld();
-                    if (!open) mask_columns(sv, v0 + j * kKeys, va, vb, vc);
+                    if (!open || bad)
+                        mask_columns(sv, v0 + j * kKeys, va, vb, vc, keeps + (unit_base / 2 + k_order(j)) % kKeeps * KEEP);
                     const float mt = row_max<kKeys>(sv) * p.scale_log2;
                     const bool over = mt > m + kRescaleSlack;
                     const bool rescale = __any_sync(0xffffffffu, over);
@@ -825,7 +860,6 @@ chunk_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                         (p.split || x == 0 || j >= u.nk[0])) {
                         // ring position of V_j: behind the K_0s and 2 j tiles of this stream, and
                         // what the other stream has passed
-                        const int sn1 = u.sn[1];
                         uint32_t fv = unit_base + 1 + 2 * j + (sn1 > 0 ? 1 + min(j, sn1) + min(j, sn1 - 1) : 0);
                         if (p.split && x == 1) fv += j + 1 < u.sn[0] ? 2 : 1;
                         if (!mbar_wait(bars + L::B_KVFULL + fv % R::RING, (fv / R::RING) & 1, abort_flag, p.err)) {
