@@ -102,11 +102,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4) decode_combine_kernel(c
     }
     if (!merge) return;
     const float inv = tot > 0.f ? 1.f / tot : 0.f;
+    // (a +inf among the lse, a partition whose scores are not numbers, makes tot and this NaN)
+    if (lane == 0 && p.lse_out != nullptr) p.lse_out[w] = tot == 0.f ? -INFINITY : mx + __logf(tot);
     if (p.out_f32 != nullptr) {
         float* dst = p.out_f32 + (size_t)w * D + lane * DPL;
 #pragma unroll
         for (int k = 0; k < DPL; ++k) dst[k] = acc[k] * inv;
-        if (lane == 0 && p.lse_out != nullptr) p.lse_out[w] = tot > 0.f ? mx + __logf(tot) : -INFINITY;
         return;
     }
     uint16_t* dst = p.out + (size_t)w * D + lane * DPL;
@@ -118,8 +119,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 4) decode_combine_kernel(c
     } else {
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
-    // (a +inf among the lse, a partition whose scores are not numbers, makes tot and this NaN)
-    if (lane == 0 && p.lse_out != nullptr) p.lse_out[w] = tot == 0.f ? -INFINITY : mx + __logf(tot);
 }
 
 template <int D>
