@@ -408,7 +408,8 @@ prefill_tcgen05_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_c
         auto load_pieces = [&](const int32_t* bt, int kbeg, int lk, int j) {
             const int key0 = j * kKV;
             const int npieces = (min(kKV, lk - key0) + piece - 1) / piece;
-            return lane < npieces ? __ldg(bt + ((kbeg + key0 + lane * piece) >> p.block_shift)) : kNoPiece;
+            // (a negative id may be any but kNoPiece)
+            return lane < npieces ? max(-1, __ldg(bt + ((kbeg + key0 + lane * piece) >> p.block_shift))) : kNoPiece;
         };
         // Claims run one unit ahead: the index and description of unit n + 1 are fetched
         // while unit n's copies are issued, so that the next unit's first copies do not
@@ -981,7 +982,8 @@ prefix_tiles_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         auto load_pieces = [&](const int32_t* bt, int kbeg, int lk, int j) {
             const int key0 = j * kKV;
             const int npieces = (min(kKV, lk - key0) + piece - 1) / piece;
-            return lane < npieces ? __ldg(bt + ((kbeg + key0 + lane * piece) >> p.block_shift)) : kNoPiece;
+            // (a negative id may be any but kNoPiece)
+            return lane < npieces ? max(-1, __ldg(bt + ((kbeg + key0 + lane * piece) >> p.block_shift))) : kNoPiece;
         };
         auto claim_next = [&]() -> int {
             return lane == 0 ? (idle_cta ? total : atomicAdd(p.unit_counter, 1)) : 0;
