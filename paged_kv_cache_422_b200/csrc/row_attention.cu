@@ -21,7 +21,7 @@
 // the streams, the merge and the launches); 256 contexts in a window of 1024 keys, bf16 cache:
 // 192 us, 5.5 TB/s; a context of 4 k keys alone 15 us.
 //
-// Layout.  Every warp is an independent worker: it takes items (KV head, row tile, range of
+// Layout.  Every warp is an independent worker: it takes items (KV head, range of
 // 16-key tiles of one sequence) and streams their K and V through its own ring of two shared
 // memory stages (of two tiles, e4m3) with 16-byte cp.async copies.  Chunks of up to 24 rows per
 // KV head (16 over a bf16 cache) take 2 or 3 such N = 8 row groups in one pass over the keys.  Rows that no query row of the item sees are
@@ -85,8 +85,6 @@ struct RowParams {
     int max_ctx;
     int window, sinks;           // window 0: none
     int planned;                 // items come from the plan kernel
-    int tok;                     // query tokens per row tile
-    int row_tiles;               // row tiles of the longest chunk
     int chunk;                   // 16-key tiles per partition
     int s_max;
     int max_entries;             // entries that the item table holds
@@ -119,37 +117,36 @@ __device__ __forceinline__ uint32_t seen_keys(int key0, int p, int window, int s
     return m;
 }
 
-// Row tile i of the call: (sequence, tile of its query tokens); ntok = 0 when there is none.
-struct RowTile {
+// The query tokens of sequence b, which are one item per KV head and partition; ntok = 0 when there
+// are none.
+struct RowSeq {
     int b, q0, ntok, p0;
     int tiles, ns;       // 16-key tiles that it sees, partitions
 };
-__device__ __forceinline__ RowTile row_tile(const RowParams& p, int i, bool flag) {
+__device__ __forceinline__ RowSeq row_seq(const RowParams& p, int b, bool flag) {
     const int lim = (int)min((long long)p.max_ctx, (long long)p.max_blocks * p.block_size);
-    RowTile t;
-    t.b = i / p.row_tiles;
-    const int rt = i - t.b * p.row_tiles;
-    int ctx = __ldg(p.context_lens + t.b), lq = 1;
-    t.q0 = t.b;
+    RowSeq t;
+    t.b = b;
+    int ctx = __ldg(p.context_lens + b);
+    t.ntok = 1;
+    t.q0 = b;
     bool ok = ctx >= 0 && ctx <= lim;
     if (p.cu_q != nullptr) {
-        t.q0 = __ldg(p.cu_q + t.b);
-        const int q1 = __ldg(p.cu_q + t.b + 1);
+        t.q0 = __ldg(p.cu_q + b);
+        const int q1 = __ldg(p.cu_q + b + 1);
         ok = ok && t.q0 >= 0 && q1 >= t.q0 && q1 <= p.total_q && q1 - t.q0 <= p.max_q && q1 - t.q0 <= ctx;
-        lq = ok ? q1 - t.q0 : 0;   // a bad sequence's rows are left unwritten
+        t.ntok = ok ? q1 - t.q0 : 0;   // a bad sequence's rows are left unwritten
     } else {
         ctx = min(max(ctx, 0), lim);
     }
-    if (!ok && flag && rt == 0) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
-    t.ntok = min(p.tok, lq - rt * p.tok);
-    t.q0 += rt * p.tok;
-    t.p0 = ctx - lq + rt * p.tok;
+    if (!ok && flag) flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
+    t.p0 = ctx - t.ntok;
     t.tiles = t.ntok > 0 && t.p0 >= 0 ? tile_range(t.p0, t.p0 + t.ntok - 1, p.window, p.sinks).count : 0;
     t.ns = t.ntok > 0 ? max(1, (t.tiles + p.chunk - 1) / p.chunk) : 0;
     return t;
 }
 // Its partitions of the full size; the last one is shorter when there is one more.
-__device__ __forceinline__ int full_parts(const RowParams& p, const RowTile& t) {
+__device__ __forceinline__ int full_parts(const RowParams& p, const RowSeq& t) {
     return t.ns - (t.tiles < t.ns * p.chunk ? 1 : 0);
 }
 
@@ -166,22 +163,21 @@ __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
     if (p.cu_q != nullptr)
         for (int i = tid; i < p.total_q; i += blockDim.x) p.nsplit[i] = 0;
     __syncthreads();
-    auto tile = [&](int i, bool flag) { return row_tile(p, i, flag); };
     // (cumulative lengths that run backwards can claim rows twice, and so more entries than
     // the table has room for: what does not fit is dropped and flagged)
-    auto put = [&](int at, const RowTile& t, int s) {
+    auto put = [&](int at, const RowSeq& t, int s) {
         if (at >= p.max_entries) return;
         p.items[2 * at] = make_int4(t.b, s | (t.ns << 16), t.q0, t.ntok);
         p.items[2 * at + 1] = make_int4(t.p0, s * p.chunk, min(t.tiles, (s + 1) * p.chunk), 0);
     };
     int carry = 0;
-    const int n = p.batch * p.row_tiles;
+    const int n = p.batch;
     for (int base = 0; base < n; base += blockDim.x) {
         const int i = base + tid;
-        RowTile t{};
+        RowSeq t{};
         int nfull = 0;
         if (i < n) {
-            t = tile(i, true);
+            t = row_seq(p, i, true);
             if (t.ns > 0) {
                 for (int k = 0; k < t.ntok; ++k) p.nsplit[t.q0 + k] = t.ns;
                 const int last = t.tiles - (t.ns - 1) * p.chunk;
@@ -202,7 +198,7 @@ __global__ void __launch_bounds__(1024) row_plan_kernel(const RowParams p) {
     if (tid < kLengthClasses) s_cls[cls] = carry + e;
     __syncthreads();
     for (int i = tid; i < n; i += blockDim.x) {
-        const RowTile t = tile(i, false);
+        const RowSeq t = row_seq(p, i, false);
         if (t.ns == 0) continue;
         const int last = t.tiles - (t.ns - 1) * p.chunk;
         if (last == p.chunk) continue;
@@ -303,8 +299,8 @@ row_attention_kernel(const RowParams p) {
     const int nwarps = gridDim.x * kRowWarps;
     int nx_item = blockIdx.x * kRowWarps + warp;
     // A call whose items fit one round has no plan kernel, which would cost 5 us of its 15 to 100:
-    // every CTA counts the row tiles' partitions itself, a row tile per thread.  Items are the
-    // full partitions of all row tiles, then the shorter last ones, each for every KV head.  (With
+    // every CTA counts the sequences' partitions itself, a sequence per thread.  Items are the
+    // full partitions of all sequences, then the shorter last ones, each for every KV head.  (With
     // several rounds the plan's order and dynamic claims are worth more than its time: 64 contexts
     // of 0.5 to 4 k keys 72 us with it, 78 without.)
     __shared__ int s_full[kRowWarps * 32], s_rest[kRowWarps * 32], s_scan[32];
@@ -314,8 +310,8 @@ row_attention_kernel(const RowParams p) {
         total_items = __ldcg(p.counter + 1);
     } else {
         int full = 0, rest = 0, total_rest = 0;
-        if ((int)threadIdx.x < p.batch * p.row_tiles) {
-            const RowTile r = row_tile(p, threadIdx.x, blockIdx.x == 0);
+        if ((int)threadIdx.x < p.batch) {
+            const RowSeq r = row_seq(p, threadIdx.x, blockIdx.x == 0);
             full = full_parts(p, r);
             rest = r.ns - full;
         }
@@ -324,7 +320,7 @@ row_attention_kernel(const RowParams p) {
         __syncthreads();
         total_items = (total_full + total_rest) * p.hkv;
     }
-    // item c (of one KV head) without a plan: its row tile is the last one with at most c
+    // item c (of one KV head) without a plan: its sequence is the last one with at most c
     // partitions before it
     auto find = [&](int c) {
         const bool rest = c >= total_full;
@@ -333,7 +329,7 @@ row_attention_kernel(const RowParams p) {
         int i = -1;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) i += __popc(__ballot_sync(0xffffffffu, before[32 * w + lane] <= k));
-        const RowTile r = row_tile(p, i, false);
+        const RowSeq r = row_seq(p, i, false);
         const int s = rest ? r.ns - 1 : k - before[i];
         it_a = make_int4(r.b, s | (r.ns << 16), r.q0, r.ntok);
         it_b = make_int4(r.p0, s * p.chunk, min(r.tiles, (s + 1) * p.chunk), 0);
@@ -979,8 +975,7 @@ cudaError_t launch_rows(const RowParams& p, long long max_items, cudaStream_t st
 }
 
 struct RowGeometry {
-    int tok, row_tiles, nt, chunk, s_max;
-    long long tiles;     // bound on (sequence, row tile) pairs
+    int nt, chunk, s_max;
     size_t counter, nsplit, items, lse_part, o_part, total;
 };
 
@@ -988,7 +983,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // 16-key tiles per partition, from host-side bounds only (a captured call keeps its launches and
 // its workspace, and a sequence's partitions do not depend on the others' lengths).  `pairs`
-// row tiles times KV heads see `seen` tiles each at most.
+// sequences times KV heads see `seen` tiles each at most.
 //  - Up to a quarter as many pairs as warps: as many partitions as keep every item in one round,
 //    less a twelfth for lengths that the host does not know (8 contexts of 32 k keys in 8 bits: 24
 //    partitions each 107 us, 27 109, 30, where a second round begins, 146, 64 124; 40 of 4 k: 5
@@ -1015,25 +1010,22 @@ int row_chunk_tiles(long long pairs, long long seen, int nt, int num_splits) {
 RowGeometry row_geometry(int batch, int total_q, int max_q, int hq, int hkv, int head_dim, int max_ctx,
                          int window, int sinks, int num_splits) {
     RowGeometry r{};
-    const int group = std::max(1, hq / hkv);
-    r.nt = max_q * group <= 8 ? 1 : max_q * group <= 16 ? 2 : 3;
-    r.tok = std::max(1, std::min(max_q, 8 * r.nt / group));
-    r.row_tiles = std::max(1, (max_q + r.tok - 1) / r.tok);
-    r.tiles = std::min((long long)batch * r.row_tiles, (long long)batch + total_q / r.tok);
-    // 16-key tiles that a row tile can see
+    const int rows = max_q * std::max(1, hq / hkv);   // of a KV head: at most 24, longer chunks go to the tiles
+    r.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 3;
+    // 16-key tiles that a sequence's tokens can see
     long long seen = ((long long)std::max(0, max_ctx) + kTileKeys - 1) / kTileKeys;
     if (window > 0)
-        seen = std::min(seen, ((long long)window + r.tok + kTileKeys - 2) / kTileKeys + 1 +
+        seen = std::min(seen, ((long long)window + std::max(1, max_q) + kTileKeys - 2) / kTileKeys + 1 +
                                   ((long long)sinks + kTileKeys - 1) / kTileKeys);
     seen = std::max(1LL, seen);
-    r.chunk = row_chunk_tiles(r.tiles * hkv, seen, r.nt, num_splits);
+    r.chunk = row_chunk_tiles((long long)batch * hkv, seen, r.nt, num_splits);
     // the partition index travels in 15 bits
     r.chunk = (int)std::max<long long>(r.chunk, (seen + 32766) / 32767);
     r.s_max = (int)((seen + r.chunk - 1) / r.chunk);
     size_t off = 256;
     r.counter = 0;
     r.nsplit = off; off = align256(off + sizeof(int32_t) * (size_t)total_q);
-    r.items = off; off = align256(off + 2 * sizeof(int4) * (size_t)r.tiles * r.s_max);
+    r.items = off; off = align256(off + 2 * sizeof(int4) * (size_t)batch * r.s_max);
     r.lse_part = off; off = align256(off + (r.s_max > 1 ? sizeof(float) * (size_t)total_q * hq * r.s_max : 0));
     r.o_part = off; off = align256(off + (r.s_max > 1 ? sizeof(float) * (size_t)total_q * hq * r.s_max * head_dim : 0));
     r.total = off;
@@ -1054,7 +1046,8 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
         set_error("workspace too small: %zu bytes given, %zu needed", c.workspace_bytes, r.total);
         return NVPA_ERR_WORKSPACE_TOO_SMALL;
     }
-    if (r.tiles * r.s_max * c.hkv > 0x7fffffffLL / 2 || (long long)c.batch * r.row_tiles > 0x7fffffffLL / 2) {
+    const long long max_items = (long long)c.batch * r.s_max * c.hkv;
+    if (max_items > 0x7fffffffLL / 2) {
         set_error("more than 2^30 work items");
         return NVPA_ERR_UNSUPPORTED;
     }
@@ -1090,18 +1083,15 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
     // (a window as long as the longest context hides nothing)
     p.window = c.window >= c.max_context_len ? 0 : c.window;
     p.sinks = std::min(c.num_sinks, c.max_context_len);
-    p.max_entries = (int)(r.tiles * r.s_max);
-    p.planned = (long long)c.batch * r.row_tiles > kRowWarps * 32 ||
-                r.tiles * r.s_max * c.hkv > row_resident_warps(r.nt);
-    p.tok = r.tok;
-    p.row_tiles = r.row_tiles;
+    p.max_entries = c.batch * r.s_max;
+    p.planned = c.batch > kRowWarps * 32 || max_items > row_resident_warps(r.nt);
     p.chunk = r.chunk;
     p.s_max = r.s_max;
     p.scale_log2 = c.scale * kLog2e;
     cudaError_t e = cudaSuccess;
     if (p.planned) {
         // (its time is barriers and load latency: fewer warps where they suffice, 0.4 us)
-        row_plan_kernel<<<1, (long long)c.batch * r.row_tiles <= 256 ? 256 : 1024, 0, stream>>>(p);
+        row_plan_kernel<<<1, c.batch <= 256 ? 256 : 1024, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_failure(e, "row attention plan launch");
         count_launches(1);
@@ -1110,7 +1100,6 @@ nvpa_status_t run_row_attention(const WindowCall& c, cudaStream_t stream) {
         e = cudaMemsetAsync(p.nsplit, 0, sizeof(int32_t) * (size_t)c.total_q, stream);
         if (e != cudaSuccess) return cuda_failure(e, "row attention memset");
     }
-    const long long max_items = r.tiles * r.s_max * c.hkv;
     const bool fp8 = c.k_scales != nullptr;
     e = cudaErrorInvalidValue;
 #define NVPA_CASE(DD, FF, NN) \
