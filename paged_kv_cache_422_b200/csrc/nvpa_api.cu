@@ -481,9 +481,11 @@ nvpa_status_t nvpa_paged_decode_attention_window(
 
 // Which kernel a chunk call takes: few query rows per KV head (tokens times heads of its group)
 // go to the row kernel, which reads the keys once for 16 rows (24 of an e4m3 cache); more go to
-// the 128-row tiles.  (8 contexts of 8 k keys, 32 / 8 heads, e4m3 cache: 16 rows 50 us by rows
-// and 71 by tiles, 20 rows 58 and 71, 32 rows in two passes 106 and 71; bf16 cache: 12 rows 65
-// and 62, 20 rows 75 and 62.)
+// the 128-row tiles.  (32 / 8 heads, e4m3 cache: 8 contexts of 8 k keys, 24 rows 56 us by rows and
+// 73 by tiles, 64 contexts of 0.5 to 4 k 128 and 163, one context of 8 k 27.7 and 25.6 to 29.  bf16
+// cache: 8 contexts of 8 k, 8 rows 59 and 61, 12 rows 63 and 62, 16 rows 64 and 62, 20 rows 75 and
+// 62; of 256 keys, 16 rows 19.0 and 19.6; 64 windows of 1024 keys 90 and 80.  From 9 to 16 bf16 rows
+// neither form is ahead by much, and the row kernel rounds the weights to 16 bits, not 8.)
 constexpr int kRowKernelRows = 16, kRowKernelRowsE4m3 = 24;
 static bool chunk_on_tiles(int max_seqlen_q, int num_q_heads, int num_kv_heads, bool e4m3) {
     return (long long)max_seqlen_q * (num_q_heads / num_kv_heads) > (e4m3 ? kRowKernelRowsE4m3 : kRowKernelRows);

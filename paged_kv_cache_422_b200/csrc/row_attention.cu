@@ -994,7 +994,11 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Four tiles at least: shorter items cost more than the warps they fill; and up to 8 tiles stay
 // whole, since that saves the combine and a chunk's plan (one context of 128 keys 13.7 us, two
 // partitions 14.7; 4 chunks of 5 tokens at 128 keys 17.5 and 20.1, at 256 keys 23.4 and 20.1).
-constexpr long long row_resident_warps(int nt) { return 148LL * kRowWarps * (nt == 1 ? 3 : 2); }   // on a B200
+//
+// Warps that a B200 holds at head_dim 128: 3 CTAs per SM for 8 rows and 2 for more.  (At head_dim 64
+// the register file has room for 4, and 3 with 16 e4m3 rows, so that "one round" leaves some of the
+// warps idle there; partitions for them have not been measured.)
+constexpr long long row_resident_warps(int nt) { return 148LL * kRowWarps * (nt == 1 ? 3 : 2); }
 int row_chunk_tiles(long long pairs, long long seen, int nt, int num_splits) {
     if (num_splits > 0) return (int)std::max(1LL, (seen + num_splits - 1) / num_splits);
     const long long warps = row_resident_warps(nt);
