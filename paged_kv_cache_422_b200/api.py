@@ -343,17 +343,20 @@ def _expect(t, dtype, name, shape, index):
 
 
 def _expect_rows(t, name, shape, index):
-    """As _expect for bf16 rows [N, Hkv, D] whose token stride may exceed Hkv * D."""
+    """As _expect for bf16 rows [N, Hkv, D] whose token stride may exceed Hkv * D; the token stride.
+    (Of a dimension of size 1 any stride will do.)"""
+    n, hkv, d = shape
     if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape
             and t.get_device() == index and t.is_contiguous()):
-        return
+        return hkv * d
     _need(t, _BF16, name, 3)
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if shape[0] and (t.stride(2) != 1 or t.stride(1) != shape[2]):
+    if n and (t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d)):
         raise ValueError(f"{name}: heads and dims of a token must be contiguous")
+    return t.stride(0) if n > 1 else hkv * d
 
 
 def _flag_ptr(err_flag, index):
@@ -444,11 +447,11 @@ def store_kvcache_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, 
         raise TypeError("k_scales and v_scales are required")
     _expect(slot_mapping, _I32, "slot_mapping", 1, index)
     n = slot_mapping.shape[0]
-    _expect_rows(k, "k", (n, hkv, d), index)
-    _expect_rows(v, "v", (n, hkv, d), index)
+    k_stride = _expect_rows(k, "k", (n, hkv, d), index)
+    v_stride = _expect_rows(v, "v", (n, hkv, d), index)
     _call(
         "nvpa_store_kvcache_fp8", index,
-        k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0), k_cache.data_ptr(),
+        k.data_ptr(), v.data_ptr(), k_stride, v_stride, k_cache.data_ptr(),
         v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(),
         n, hkv, d, nb, bs, _flag_ptr(err_flag, index), _raw_stream(index, stream))
 
