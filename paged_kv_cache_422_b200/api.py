@@ -511,9 +511,9 @@ def _workspace(workspace, like, index, stream, size, *args):
 
 def paged_decode_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_context_len,
                                        block_size, window=0, num_sinks=0, num_splits=0) -> int:
-    return lib().nvpa_paged_decode_window_workspace_size(
-        batch, num_q_heads, num_kv_heads, head_dim, *_c_ints(
-            max_context_len, block_size, window, num_sinks, num_splits))
+    return lib().nvpa_paged_decode_window_workspace_size(*_c_ints(
+        batch, num_q_heads, num_kv_heads, head_dim, max_context_len, block_size, window, num_sinks,
+        num_splits))
 
 
 def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_lens, max_context_len,
@@ -547,9 +547,9 @@ def paged_decode_attention_window(q, k_cache, v_cache, block_tables, context_len
 def chunk_attention_workspace_size(batch, total_q, num_q_heads, num_kv_heads, head_dim,
                                    max_seqlen_q, max_context_len, block_size, window=0,
                                    num_sinks=0, num_splits=0) -> int:
-    return lib().nvpa_chunk_attention_workspace_size(
-        batch, total_q, num_q_heads, num_kv_heads, head_dim, *_c_ints(
-            max_seqlen_q, max_context_len, block_size, window, num_sinks, num_splits))
+    return lib().nvpa_chunk_attention_workspace_size(*_c_ints(
+        batch, total_q, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_context_len,
+        block_size, window, num_sinks, num_splits))
 
 
 def chunk_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q,
