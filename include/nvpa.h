@@ -425,7 +425,8 @@ nvpa_status_t nvpa_gather_kv(void* dst, const void* cache,
  *   v_scales        aligned (written): the scale of slot b * block_size + row and head h is
  *                   byte (b * num_kv_heads + h) * block_size + row.
  *   slot_mapping    as in nvpa_store_kvcache (-1: padding; out of range: flagged, skipped;
- *                   two tokens with the same slot: undefined which row lands).
+ *                   two tokens with the same slot: undefined what the row holds, one's codes
+ *                   with the other's scale among it).
  *   head_dim        64 or 128; block_size 16, 32, 64, 128 or 256.
  * Errors: NVPA_ERR_INVALID_ARG, NVPA_ERR_UNSUPPORTED as for nvpa_store_kvcache.
  */
@@ -443,6 +444,7 @@ nvpa_status_t nvpa_store_kvcache_fp8(const void* k, const void* v, int64_t k_tok
  *   dst             bf16 [total_k, num_kv_heads, head_dim] (written).  Rows whose block id is
  *                   out of range are zeroed and flagged; rows from cu_seqlens_k[batch] on
  *                   are left as they are and flagged (NVPA_FLAG_BAD_LENGTH).
+ *   batch, total_k  >= 0; a call with either 0 does nothing.
  */
 nvpa_status_t nvpa_gather_kv_fp8(void* dst, const void* cache, const uint8_t* scales,
                                  const int32_t* block_tables, int max_blocks_per_seq,
@@ -483,6 +485,12 @@ size_t nvpa_paged_decode_window_workspace_size(int batch, int num_q_heads, int n
  * (bf16 cache) with a weight of at least 2^-100 of the row's largest makes its dim infinite, or NaN
  * beside one of the other sign.  A sequence's result depends on its own rows and on the call's
  * host-side arguments only, not on the other sequences.
+ *
+ * Over a bf16 cache without a window it computes what nvpa_paged_decode_attention computes.  That
+ * one is the faster for large batches of groups of 1 and 2 (64 contexts of 0.5 to 4 k keys, 8 KV
+ * heads of 128: 106 and 111 us against 113 and 114; heads of 64: 69 against 79), this one for
+ * groups of 4 and more (125 against 116), for long contexts (8 of 32 k: 193 to 201 against 181)
+ * and for short or few ones (16 of 256 keys: 21 against 17).
  */
 nvpa_status_t nvpa_paged_decode_attention_window(
     void* out, float* lse_out, const void* q, const void* k_cache, const void* v_cache, int cache_type,
@@ -509,11 +517,19 @@ size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_hea
  * block-table entries are read, is as for nvpa_paged_decode_attention_window.  When there
  * are few query rows the keys are cut into partitions that run in parallel and are merged
  * with their log-sum-exp weights.  Up to 16 query rows (tokens times query heads) per KV head,
- * 24 over an e4m3 cache, run as the decode does; longer chunks on 128-row tensor-core tiles,
- * whose softmax weights are rounded to 8 significant bits (bf16).  Keys that no query row of the
- * call sees never show in a result, whatever their rows hold; a key that some of a sequence's
+ * 24 over an e4m3 cache, run as the decode does, with its rounding; longer chunks on 128-row
+ * tensor-core tiles, whose softmax weights are rounded to 8 significant bits (bf16).  max_seqlen_q
+ * decides for the whole call, so a bound above the longest chunk can cost bits, and single tokens
+ * beside a long chunk each take a tile: over an e4m3 cache they are faster in a call of their own
+ * (a chunk of 512 tokens and 63 single ones over 4 to 8 k keys: 466 us in one call, 107 + 168 in
+ * two; bf16 cache 388 and 96 + 276).  Keys that no query row of the call sees never show in a result, whatever their rows hold; a key that some of a sequence's
  * query rows see may, where its value is not finite, show in that sequence's other rows too
  * (as 0 times it).
+ *
+ * Over a bf16 cache without a window it computes what nvpa_varlen_prefill_attention computes, and is
+ * the one to call for chunks over long contexts (8 of 512 tokens over 4 to 8 k keys: 456 us against
+ * 580; 8 of 32: 74 against 194); whole prompts take either (32 of 64 to 2048 tokens: 272 and 282
+ * us), with heads of 64 the prefill (256 and 226).
  *
  *   out             bf16 [total_q, num_q_heads, head_dim] (written); rows from
  *                   cu_seqlens_q[batch] on are left as they are.

@@ -5,8 +5,9 @@
 // b - 127 = max(-118, ceil(log2(amax / 448))), so that no finite value saturates.  A power
 // of two keeps the relative precision of the floating-point codes that any other scale
 // would give, and makes reading back exact: a code has 4 significant bits, so c * 2^e is a
-// bf16 value (and an fp16 value before the scale).  -118 is the smallest exponent for which
-// every code, subnormals included, is still a multiple of the smallest bf16 magnitude.
+// bf16 value (and an fp16 value before the scale).  From -118 on that holds for every code,
+// subnormals included: codes are multiples of 2^-9, their values of 2^-127, 2^6 above the
+// smallest bf16 magnitude; rows below 448 * 2^-118 lose relative precision instead.
 #pragma once
 
 #include <cuda_fp16.h>

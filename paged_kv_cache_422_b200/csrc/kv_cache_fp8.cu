@@ -5,8 +5,9 @@
 // Both are bound by HBM bandwidth (3 bytes per value: 2 of bf16, 1 of e4m3), so each value
 // is loaded once with 16-byte loads and the row's maximum never leaves the registers: D / 16
 // lanes hold one row (16 values each), log2(D / 16) shuffles give its largest magnitude.
-// Measured with 8 heads of 128: 24594 tokens stored in 25.2 us (6.0 TB/s, 0.92 of the copy
-// bandwidth), 33 k rows read back in 18.7 us (5.7 TB/s, 0.88).
+// Measured with 8 heads of 128, inputs that change from call to call: 24594 tokens stored in 28.8 us
+// (5.3 TB/s, 0.80 of the copy bandwidth), 33 k rows read back in 22.8 us (4.7 TB/s, 0.72).  Repeats on
+// the same buffers, whose lines are partly in L2, take 25.2 and 18.7.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(256) store_fp8_kernel(const StoreFp8Params p) 
 // (sequence, block id, codes), so the slots of the next tile's rows are looked up, a row per
 // thread, while this tile's codes are on their way.
 constexpr int kGatherThreads = 256, kGatherPer = 2, kGatherChunks = kGatherThreads * kGatherPer;
-// Blocks per SM: as many as fit.  (33 k rows of 8 heads of 128: 18.7 us; chunks of 8 codes, whose
+// Blocks per SM: as many as fit.  (Repeats of 33 k rows of 8 heads of 128: 18.7 us; chunks of 8 codes, whose
 // address work is the same, 21.3, and with 4 or 6 blocks 24.4 and 23.5; four chunks a thread in
 // 6 blocks 19.1.)
 constexpr int kGatherBlocks = 8;

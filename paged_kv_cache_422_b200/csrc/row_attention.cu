@@ -16,10 +16,10 @@
 // it take about 670 warp instructions for any G up to 8, a third of them the conversion of its
 // codes.  (tcgen05 needs M = 64 or 128 rows of accumulators in TMEM per product, a single
 // warp's stream of keys has no use for it.)
-// Measured: 8 contexts of 32 k keys, 32 / 8 heads of 128, e4m3 cache: 104 us, 5.2 TB/s (0.80 of
+// Measured: 8 contexts of 32 k keys, 32 / 8 heads of 128, e4m3 cache: 105 us, 5.1 TB/s (0.79 of
 // the copy bandwidth; the marginal rate of more contexts is 6.3 TB/s, the rest is the start of
 // the streams, the merge and the launches); 256 contexts in a window of 1024 keys, bf16 cache:
-// 192 us, 5.5 TB/s; a context of 4 k keys alone 15 us.
+// 194 us, 5.5 TB/s; a context of 4 k keys alone 15 us.
 //
 // Layout.  Every warp is an independent worker: it takes items (KV head, range of
 // 16-key tiles of one sequence) and streams their K and V through its own ring of two shared
