@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(256) gather_kv_kernel(
         const int k0 = __ldg(cu_seqlens_k + lo), k1 = __ldg(cu_seqlens_k + lo + 1);
         const int pos = (int)(row - k0);
         uint4* d = dst + row * row16;
-        if (row < k0 || row >= k1 || (long long)pos >= (long long)max_blocks * block_size) {
+        // (a negative start comes first: the position behind it may have overflowed)
+        if (k0 < 0 || row < k0 || row >= k1 || (long long)pos >= (long long)max_blocks * block_size) {
             if (lane == 0) flag_error(err_flag, NVPA_FLAG_BAD_LENGTH);
             continue;
         }

@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Gather
             const int k0 = __ldg(p.cu + lo), k1 = __ldg(p.cu + lo + 1);
             const int pos = row - k0;
             int slot = kNoRow;
-            if (row < k0 || row >= k1 || (long long)pos >= (long long)p.max_blocks * p.block_size) {
+            // (a negative start comes first: the position behind it may have overflowed)
+            if (k0 < 0 || row < k0 || row >= k1 || (long long)pos >= (long long)p.max_blocks * p.block_size) {
                 flag_error(p.err, NVPA_FLAG_BAD_LENGTH);
             } else {
                 const int blk = checked_block(p.block_tables + (size_t)lo * p.max_blocks, pos, p.block_shift,
