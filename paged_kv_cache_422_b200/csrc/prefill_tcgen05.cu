@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillParams 
         const int k0 = __ldg(p.cu_k + i), k1 = __ldg(p.cu_k + i + 1);
         lq = q1 - q0;
         lk = k1 - k0;
-        return q0 >= 0 && lq >= 0 && lk >= lq && lq <= p.max_q && lk <= p.max_k && lk <= cap &&
+        // (in this order: the difference of bounds that run backwards may have overflowed)
+        return q0 >= 0 && q1 >= q0 && k1 >= k0 && lk >= lq && lq <= p.max_q && lk <= p.max_k && lk <= cap &&
                q1 <= p.total_q;
     };
     auto bucket = [&](int nkv) { return min(nkv, kPlanBuckets - 1); };

@@ -32,6 +32,20 @@ def test_gather(cuda_device, fp8, cu):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("cu_q,cu_k", [([HIGH, LOW], [0, 4]), ([0, 2], [HIGH, LOW]), ([HIGH, LOW], [HIGH, LOW]),
+                                       ([LOW, HIGH], [LOW, HIGH]), ([0, 2], [LOW, HIGH])])
+def test_prefill(cuda_device, cu_q, cu_k):
+    dev = cuda_device
+    cache = torch.ones((4, 16, 2, 64), dtype=torch.bfloat16, device=dev)
+    q = torch.ones((2, 4, 64), dtype=torch.bfloat16, device=dev)
+    out, lse = torch.full_like(q, 5.0), torch.full((2, 4), 5.0, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    nvpa.varlen_prefill_attention(q, cache, cache, i32([[1, 2]], dev), i32(cu_q, dev), i32(cu_k, dev), 2, 20, 0.1, out=out,
+                                  lse=lse, err_flag=err)
+    assert err.item() == nvpa.NVPA_FLAG_BAD_LENGTH
+    assert bool((out == 5.0).all()) and bool((lse == 5.0).all())
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("max_q", [2, 40])
 @pytest.mark.parametrize("cu", [[HIGH, LOW, 2], [LOW, HIGH, 2], [0, LOW, HIGH], [LOW, LOW, LOW], [HIGH, HIGH, LOW]])
