@@ -522,9 +522,9 @@ size_t nvpa_chunk_attention_workspace_size(int batch, int total_q, int num_q_hea
  * decides for the whole call, so a bound above the longest chunk can cost bits, and single tokens
  * beside a long chunk each take a tile: over an e4m3 cache they are faster in a call of their own
  * (a chunk of 512 tokens and 63 single ones over 4 to 8 k keys: 466 us in one call, 107 + 168 in
- * two; bf16 cache 388 and 96 + 276).  Keys that no query row of the call sees never show in a result, whatever their rows hold; a key that some of a sequence's
- * query rows see may, where its value is not finite, show in that sequence's other rows too
- * (as 0 times it).
+ * two; bf16 cache 388 and 96 + 276).  Keys that no query row of the call sees never show in a
+ * result, whatever their rows hold; a key that some of a sequence's query rows see may, where its
+ * value is not finite, show in that sequence's other rows too (as 0 times it).
  *
  * Over a bf16 cache without a window it computes what nvpa_varlen_prefill_attention computes, and is
  * the one to call for chunks over long contexts (8 of 512 tokens over 4 to 8 k keys: 456 us against

@@ -36,9 +36,9 @@
 //   P^T (B of O^T): the scores lie with keys in rows; movmatrix transposes 8 x 8 tiles.
 // Rounding: an e4m3 code is exact in fp16; q is scaled by a power of two per row to [2^14, 2^15)
 // for its largest element and rounded to fp16 (bf16 has 8 significant bits: exact for elements
-// down to 2^-31 of the largest, and off by 2^-39 of it at most).  Weights are fp16 for the e4m3 cache (2^-11 relative)
-// and a sum of two bf16 for the bf16 cache, whose values are used as they are: its upper half cut
-// off (2^-7) and the rest rounded (2^-9 of it), 2^-16 in all.
+// down to 2^-31 of the largest, and off by 2^-39 of it at most).  Weights are fp16 for the e4m3
+// cache (2^-11 relative) and a sum of two bf16 for the bf16 cache, whose values are used as they
+// are: its upper half cut off (2^-7) and the rest rounded (2^-9 of it), 2^-16 in all.
 // The fp16 weight includes the value's 2^e and is taken relative to 2^-7 of the largest such
 // weight (a running maximum of its own beside the softmax's), so a scale of any size does not
 // overflow.  fp16 holds w = p 2^(e - gap) only to 2^-25 (p: the softmax weight relative to its
